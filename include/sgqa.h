@@ -251,6 +251,124 @@ sgqa_status sgqa_sparse_attn_paged(const sgqa_params* p, int64_t num_seqs, int64
                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The 8-bit K/V cache.  K and V of every token are held as OCP FP8 E4M3 codes
+ * with one FP32 scale for the eight tokens of a block in one group's K (and
+ * one for its V); half the bytes of the BF16 caches, for the cache's size and
+ * for the decode gather.  block_size 8 only (others return
+ * SGQA_ERR_UNSUPPORTED); cache_cap is a multiple of 8.
+ *
+ * kv8      : [S, cache_cap / 8, G, 2 (K, V), 8 tokens, D] uint8 E4M3 codes
+ *            (16-byte aligned): one group's K and V of a block are contiguous
+ * kv_scale : [S, cache_cap / 8, G, 2 (K, V)] fp32 (8-byte aligned); the value
+ *            of a code is code * scale
+ * tail     : [S, 2 (K, V), 8, G, D] bf16 (16-byte aligned): the rows of the
+ *            block that is not complete yet
+ *
+ * sgqa_kv_append_q8 writes the K/V rows of positions [pos0, pos0 + n).  Every
+ * block they touch is quantised from its BF16 rows: the scale is the smallest
+ * power of two (at least 2^-100) that brings the largest magnitude among the
+ * block's rows so far to at most 448, the code E4M3_rne(x / scale).  Rows of
+ * the last block that do not exist yet get code 0.  A block begun by an
+ * earlier call takes its older rows from `tail` and is quantised again, so
+ * the cache depends on the rows alone, not on how they were cut into calls.
+ * `tail` is left with the rows of block floor((pos0 + n) / 8); it may be NULL
+ * where both pos0 and pos0 + n are multiples of 8.  A block whose K (or V)
+ * holds an infinity or NaN gets scale NaN and codes 0 there: every query that
+ * attends it reads NaN, no other is touched.
+ *
+ * k, v : [S, n, G, D] bf16, the new rows (not the whole caches)
+ */
+sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, int64_t pos0, int64_t n,
+                              const void* k, const void* v, void* tail, uint8_t* kv8, float* kv_scale,
+                              void* stream);
+
+/*
+ * sgqa_sparse_attn_gated over the 8-bit cache.  Attention of the values
+ * code * scale: a query's current block has one scale for all of its tokens
+ * that are in the cache, the query's later ones among them.  Query and softmax
+ * weights are not rounded to 8 bits (each is carried as a sum of two E4M3
+ * values); sums and softmax statistics are FP32.
+ *
+ * gate : [S, nq, G*Hg] bf16 gate logits, or NULL (no gate)
+ * acc  : [S, cache_cap / 8] int64, or NULL.  Accumulated attention weight of
+ *        every block in units of 2^-32: the call adds the softmax weights (before
+ *        the gate) that its queries' heads, of all groups, give to the block's
+ *        tokens.  Integer sums: their order does not matter.  NaN weights add 0.
+ * sel ids must be strictly ascending and below floor(t/8); others are left out
+ * and reported by sgqa_check as SGQA_ERR_DEVICE.
+ * kv_scale: as sgqa_kv_append_q8 writes it: positive (or NaN), at least 2^-100.
+ * Rows of a block at positions >= cache_len must not hold the E4M3 NaN codes
+ * 0x7F and 0xFF (sgqa_kv_append_q8 writes code 0 there).
+ * workspace: sgqa_workspace_size_q8 bytes, 256-byte aligned; calls of at most 32
+ *        queries per sequence without acc need none (NULL, 0).
+ * Other arguments and errors as sgqa_sparse_attn_gated.
+ *
+ * sgqa_workspace_size_q8: bytes that serve sgqa_index_topk, sgqa_sparse_attn_q8
+ * and sgqa_forward_q8 calls of at most nq queries per sequence at contexts up to
+ * max_ctx; pure host computation.
+ */
+sgqa_status sgqa_workspace_size_q8(const sgqa_params* p, int64_t num_seqs, int64_t nq, int64_t max_ctx,
+                                   size_t* bytes);
+sgqa_status sgqa_sparse_attn_q8(const sgqa_params* p, int64_t num_seqs, int64_t q_pos0, int64_t nq, const void* q,
+                                int64_t cache_cap, int64_t cache_len, const uint8_t* kv8, const float* kv_scale,
+                                const int32_t* sel, const int32_t* sel_count, const void* gate, int64_t* acc,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The whole hot path over the 8-bit cache: merge the blocks that this call's
+ * tokens complete, append their K/V rows (k, v: [S, nq, G, D] bf16, positions
+ * [q_pos0, q_pos0 + nq)), sgqa_index_topk, sgqa_sparse_attn_q8 (cache_len =
+ * q_pos0 + nq).  Arguments as above; the workspace serves every step.
+ */
+sgqa_status sgqa_forward_q8(const sgqa_params* p, int64_t num_seqs, int64_t q_pos0, int64_t nq, const void* q,
+                            const void* idx_q, const float* idx_w, int64_t cache_cap, const void* proxy_k,
+                            const void* comp_logits, const void* k, const void* v, void* tail, uint8_t* kv8,
+                            float* kv_scale, float* merged_f32, uint8_t* store, int32_t* sel, int32_t* sel_count,
+                            const void* gate, int64_t* acc, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * Eviction by accumulated attention weight, for any cache that is laid out
+ * block by block (the 8-bit cache, the BF16 caches, the store, ...).  Every
+ * sequence holds cache_len tokens: n = floor(cache_len / B) complete blocks in
+ * slots 0 .. n-1 and, unless cache_len is a multiple of B, an incomplete one in
+ * slot n.  Of the complete blocks `keep` stay: those with the largest acc,
+ * equal ones by the smaller original block number, and in any case the blocks
+ * whose original number is below `first` or among the `recent` last ones.
+ * Kept blocks in slots below `keep` stay where they are; the i-th freed slot
+ * takes the i-th kept block of the slots from `keep` on; the incomplete block
+ * goes to slot `keep`.  Afterwards the cache holds keep * B + cache_len % B
+ * tokens, and that is where the next call's q_pos0 is (positions are slots of
+ * the cache; keys carry their rotation).  Past blocks may stand in any order.
+ *
+ * acc      : [S, cache_cap / B] int64 (sgqa_sparse_attn_q8); acc_out the same for
+ *            the new slots, 0 from the last used one on; may be acc itself
+ * pos      : [S, cache_cap / B] int32 original block numbers of the slots below
+ *            pos_count (an earlier eviction's pos_out; NULL with pos_count 0); a
+ *            slot s >= pos_count holds block s + evicted
+ * evicted  : blocks of a sequence evicted by earlier calls
+ * pos_out  : [S, cache_cap / B] int32, original numbers of slots 0 .. keep-1; the
+ *            rest is left as it was; may be pos itself.  The next call takes
+ *            pos_count = keep, evicted = evicted + n - keep.
+ * arrays   : num_arrays (at most 8) device arrays [S, cache_cap / B, block_bytes];
+ *            tail_only: only the incomplete block is moved (rows that are not
+ *            read again once their block is merged: proxy keys, logits)
+ * workspace: sgqa_evict_workspace_size bytes, 256-byte aligned
+ * first + recent <= keep <= n.  Original numbers of a sequence must differ; where
+ * two are equal sgqa_check reports SGQA_ERR_DEVICE.
+ */
+typedef struct {
+  void* data;
+  int64_t block_bytes;
+  int32_t tail_only;
+} sgqa_cache_array;
+sgqa_status sgqa_evict_workspace_size(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, size_t* bytes);
+sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, int64_t cache_len, int64_t keep,
+                       int64_t first, int64_t recent, const int64_t* acc, const int32_t* pos, int64_t pos_count,
+                       int64_t evicted, int64_t* acc_out, int32_t* pos_out, const sgqa_cache_array* arrays,
+                       int32_t num_arrays, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream` and report the device status word that bounded waits
  * and device-side checks write (then clear it).  Returns SGQA_OK,
  * SGQA_ERR_TIMEOUT, SGQA_ERR_DEVICE or SGQA_ERR_CUDA.

@@ -27,6 +27,8 @@ STATUS = {0: "SGQA_OK", 1: "SGQA_ERR_INVALID_ARGUMENT", 2: "SGQA_ERR_UNSUPPORTED
 EXPORTED = ["sgqa_workspace_size", "sgqa_merge_blocks", "sgqa_index_topk", "sgqa_sparse_attn",
             "sgqa_sparse_attn_gated", "sgqa_forward", "sgqa_forward_gated", "sgqa_sparse_attn_paged",
             "sgqa_sparse_attn_noalloc",
+            "sgqa_workspace_size_q8", "sgqa_kv_append_q8", "sgqa_sparse_attn_q8", "sgqa_forward_q8",
+            "sgqa_evict_workspace_size", "sgqa_evict",
             "sgqa_set_wait_limit_ns", "sgqa_check", "sgqa_last_error", "sgqa_version", "sgqa_launch_count"]
 
 
@@ -42,6 +44,10 @@ class _Params(ctypes.Structure):
                 ("idx_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("topk", ctypes.c_int32), ("merge_in_f32", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class _CacheArray(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_bytes", ctypes.c_int64), ("tail_only", ctypes.c_int32)]
 
 
 @dataclasses.dataclass
@@ -76,6 +82,14 @@ _lib.sgqa_forward_gated.argtypes = [_P, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _
 _lib.sgqa_sparse_attn_paged.argtypes = [_P, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp,
                                         _vp, _vp, _sz, _vp]
 _lib.sgqa_sparse_attn_noalloc.argtypes = [_P, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.sgqa_workspace_size_q8.argtypes = [_P, _i64, _i64, _i64, ctypes.POINTER(_sz)]
+_lib.sgqa_kv_append_q8.argtypes = [_P, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.sgqa_sparse_attn_q8.argtypes = [_P, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _sz, _vp]
+_lib.sgqa_forward_q8.argtypes = [_P, _i64, _i64, _i64, _vp, _vp, _vp, _i64] + [_vp] * 15 + [_sz, _vp]
+_lib.sgqa_evict_workspace_size.argtypes = [_P, _i64, _i64, ctypes.POINTER(_sz)]
+_lib.sgqa_evict.argtypes = [_P, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp,
+                            ctypes.POINTER(_CacheArray), ctypes.c_int32, _vp, _sz, _vp]
 _lib.sgqa_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.sgqa_check.argtypes = [_vp]
 _lib.sgqa_last_error.restype = ctypes.c_char_p
@@ -189,6 +203,68 @@ def sgqa_sparse_attn_noalloc(p: Params, num_seqs, q_pos0, nq, q, cache_cap, cach
     _ok(_lib.sgqa_sparse_attn_noalloc(ctypes.byref(p.c()), num_seqs, q_pos0, nq, _ptr(q), cache_cap, cache_len,
                                       _ptr(k_cache), _ptr(v_cache), _ptr(sel), _ptr(sel_count), _ptr(out),
                                       _stream(stream)))
+
+
+def sgqa_workspace_size_q8(p: Params, num_seqs: int, nq: int, max_ctx: int) -> int:
+    out = _sz(0)
+    _ok(_lib.sgqa_workspace_size_q8(ctypes.byref(p.c()), num_seqs, nq, max_ctx, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_workspace_q8(p: Params, num_seqs: int, nq: int, max_ctx: int, device) -> torch.Tensor:
+    n = sgqa_workspace_size_q8(p, num_seqs, nq, max_ctx)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def sgqa_kv_append_q8(p: Params, num_seqs, cache_cap, pos0, n, k, v, tail, kv8, kv_scale, stream=None):
+    """Quantise the K/V rows of positions [pos0, pos0 + n) (k, v: [S, n, G, D] bf16) into the 8-bit cache."""
+    _ok(_lib.sgqa_kv_append_q8(ctypes.byref(p.c()), num_seqs, cache_cap, pos0, n, _ptr(k), _ptr(v), _ptr(tail),
+                               _ptr(kv8), _ptr(kv_scale), _stream(stream)))
+
+
+def sgqa_sparse_attn_q8(p: Params, num_seqs, q_pos0, nq, q, cache_cap, cache_len, kv8, kv_scale, sel, sel_count, out,
+                        workspace=None, gate=None, acc=None, stream=None):
+    """Attention over the 8-bit cache; acc ([S, cache_cap / 8] int64, units of 2^-32) gains the blocks' weights."""
+    _ok(_lib.sgqa_sparse_attn_q8(ctypes.byref(p.c()), num_seqs, q_pos0, nq, _ptr(q), cache_cap, cache_len, _ptr(kv8),
+                                 _ptr(kv_scale), _ptr(sel), _ptr(sel_count), _ptr(gate), _ptr(acc), _ptr(out),
+                                 _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                                 _stream(stream)))
+
+
+def sgqa_forward_q8(p: Params, num_seqs, q_pos0, nq, q, idx_q, idx_w, cache_cap, proxy_k, comp_logits, k, v, tail, kv8,
+                    kv_scale, merged_f32, store, sel, sel_count, out, workspace, gate=None, acc=None, stream=None):
+    """merge -> append (k, v: the call's own rows) -> index/top-k -> attention over the 8-bit cache."""
+    _ok(_lib.sgqa_forward_q8(ctypes.byref(p.c()), num_seqs, q_pos0, nq, _ptr(q), _ptr(idx_q), _ptr(idx_w), cache_cap,
+                             _ptr(proxy_k), _ptr(comp_logits), _ptr(k), _ptr(v), _ptr(tail), _ptr(kv8), _ptr(kv_scale),
+                             _ptr(merged_f32), _ptr(store), _ptr(sel), _ptr(sel_count), _ptr(gate), _ptr(acc),
+                             _ptr(out), _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                             _stream(stream)))
+
+
+def sgqa_evict_workspace_size(p: Params, num_seqs: int, cache_cap: int) -> int:
+    out = _sz(0)
+    _ok(_lib.sgqa_evict_workspace_size(ctypes.byref(p.c()), num_seqs, cache_cap, ctypes.byref(out)))
+    return out.value
+
+
+def alloc_evict_workspace(p: Params, num_seqs: int, cache_cap: int, device) -> torch.Tensor:
+    return torch.empty(max(sgqa_evict_workspace_size(p, num_seqs, cache_cap), 256), dtype=torch.uint8, device=device)
+
+
+def sgqa_evict(p: Params, num_seqs, cache_cap, cache_len, keep, first, recent, acc, pos, pos_count, evicted, acc_out,
+               pos_out, arrays, workspace, tail_arrays=(), stream=None):
+    """Keep the `keep` heaviest blocks of every sequence.  arrays: contiguous tensors whose leading dimensions are
+    (sequence, block) or (sequence, token); tail_arrays: the same, of which only the incomplete block moves."""
+    blocks = num_seqs * (cache_cap // p.block_size)
+    every = [(t, 0) for t in arrays] + [(t, 1) for t in tail_arrays]
+    for t, _ in every:
+        if not t.is_contiguous() or blocks == 0 or t.numel() * t.element_size() % blocks:
+            raise ValueError("evict: every array is contiguous and holds cache_cap / block_size blocks per sequence")
+    c = (_CacheArray * max(1, len(every)))(*[_CacheArray(t.data_ptr(), t.numel() * t.element_size() // blocks, f)
+                                             for t, f in every])
+    _ok(_lib.sgqa_evict(ctypes.byref(p.c()), num_seqs, cache_cap, cache_len, keep, first, recent, _ptr(acc), _ptr(pos),
+                        pos_count, evicted, _ptr(acc_out), _ptr(pos_out), c, len(every), _ptr(workspace),
+                        workspace.numel() if workspace is not None else 0, _stream(stream)))
 
 
 def sgqa_set_wait_limit_ns(ns: int):

@@ -17,8 +17,10 @@
 #include "attn_mma.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
+#include "evict.cuh"
 #include "index_rows.cuh"
 #include "index_tc.cuh"
+#include "kv8.cuh"
 #include "merge.cuh"
 
 namespace {
@@ -627,6 +629,71 @@ sgqa_status do_attn(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, con
   return do_attn_kv(p, S, q0, nq, q, kv, sel, sel_count, out, gate, ws, st);
 }
 
+// ---- the 8-bit K/V cache ---------------------------------------------------
+struct Q8Cache {
+  const uint8_t* kv8;
+  const float* scale;
+  int64_t blocks;  // per sequence
+};
+
+sgqa_status check_q8(const sgqa_params* p, int64_t cap) {
+  if (p->block_size != sgqa::kQ8Tok) return fail(SGQA_ERR_UNSUPPORTED, "the 8-bit K/V cache needs block_size 8");
+  if (cap % sgqa::kQ8Tok != 0) return fail(SGQA_ERR_INVALID_ARGUMENT, "cache_cap (%lld) must be a multiple of 8", (long long)cap);
+  return SGQA_OK;
+}
+
+sgqa_status do_append_q8(const sgqa_params* p, int64_t S, int64_t cap, int64_t pos0, int64_t n, const void* k,
+                         const void* v, void* tail, uint8_t* kv8, float* scale, cudaStream_t st) {
+  const int G = p->num_kv_groups;
+  const int64_t nb = (pos0 + n - 1) / sgqa::kQ8Tok - pos0 / sgqa::kQ8Tok + 1;
+  const int64_t units = S * nb * 2 * G;
+  const int64_t grid = (units + sgqa::kAppendWarps - 1) / sgqa::kAppendWarps;
+  if (grid > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "append too large for one call");
+  sgqa::kv_append_q8_kernel<<<static_cast<unsigned>(grid), sgqa::kAppendWarps * 32, 0, st>>>(
+      static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(tail), kv8,
+      scale, pos0, n, G, cap / sgqa::kQ8Tok, nb, units);
+  SGQA_LAUNCH_CHECK("kv_append_q8_kernel");
+  return SGQA_OK;
+}
+
+size_t attn_q8_ws_bytes(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
+  return 0;
+}
+
+// Workspace of sgqa_forward_q8 (its steps run in turn).
+size_t forward_q8_ws_bytes(const sgqa_params* p, int64_t S, int64_t nq, int64_t max_ctx) {
+  return std::max(index_ws_bytes_upto(p, S, nq, std::max<int64_t>(max_ctx, 1)), attn_q8_ws_bytes(p, S, nq, true));
+}
+
+sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, const void* q, const Q8Cache& c,
+                       const int32_t* sel, const int32_t* sel_count, const void* gate, int64_t* acc, void* out, void* ws,
+                       cudaStream_t st) {
+  const int64_t rows = S * nq * p->num_kv_groups;
+  if (rows > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "too many queries for one call");
+  const size_t smem = sizeof(sgqa::Q8SimpleSmem);
+  cudaFuncSetAttribute(sgqa::attn_q8_simple_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  sgqa::attn_q8_simple_kernel<<<static_cast<unsigned>(rows), sgqa::kQ8SimpleThreads, smem, st>>>(
+      static_cast<const __nv_bfloat16*>(q), c.kv8, c.scale, sel, sel_count, static_cast<const __nv_bfloat16*>(gate),
+      static_cast<__nv_bfloat16*>(out), acc, nq, p->num_kv_groups, p->topk, q0, c.blocks,
+      softmax_scale(p) * 1.4426950408889634f);
+  SGQA_LAUNCH_CHECK("attn_q8_simple_kernel");
+  return SGQA_OK;
+}
+
+// Workspace of an eviction: move lists, the moved blocks' weights and numbers, a count per sequence.
+struct EvictLayout {
+  size_t moves_off, macc_off, mpos_off, count_off, bytes;
+};
+EvictLayout evict_layout(int64_t S, int64_t slots) {
+  EvictLayout l;
+  l.moves_off = 0;
+  l.macc_off = align256(static_cast<size_t>(S * slots) * 8);
+  l.mpos_off = l.macc_off + align256(static_cast<size_t>(S * (slots + 1)) * 8);
+  l.count_off = l.mpos_off + align256(static_cast<size_t>(S * slots) * 4);
+  l.bytes = l.count_off + align256(static_cast<size_t>(S) * 4);
+  return l;
+}
+
 sgqa_status check_common(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, int64_t cap) {
   sgqa_status s = check_params(p);
   if (s != SGQA_OK) return s;
@@ -905,6 +972,173 @@ sgqa_status sgqa_sparse_attn_noalloc(const sgqa_params* p, int64_t num_seqs, int
   }
   return do_attn(p, num_seqs, q_pos0, nq, q, cache_cap, cache_len, k_cache, v_cache, sel, sel_count, out, nullptr,
                  scratch, static_cast<cudaStream_t>(stream));
+}
+
+sgqa_status sgqa_workspace_size_q8(const sgqa_params* p, int64_t num_seqs, int64_t nq, int64_t max_ctx,
+                                   size_t* bytes) {
+  g_err.clear();
+  sgqa_status s = check_params(p);
+  if (s != SGQA_OK) return s;
+  if ((s = check_q8(p, 0)) != SGQA_OK) return s;
+  if (bytes == nullptr) return fail(SGQA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  if (num_seqs < 1 || nq < 0 || max_ctx < nq) return fail(SGQA_ERR_INVALID_ARGUMENT, "bad sizes");
+  // calls of nq queries and, on the decode path, of up to 32
+  *bytes = std::max(forward_q8_ws_bytes(p, num_seqs, nq, max_ctx),
+                    forward_q8_ws_bytes(p, num_seqs, std::min(nq, kDecodeMaxNq), max_ctx));
+  return SGQA_OK;
+}
+
+sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, int64_t pos0, int64_t n,
+                              const void* k, const void* v, void* tail, uint8_t* kv8, float* kv_scale,
+                              void* stream) {
+  g_err.clear();
+  sgqa_status s = check_common(p, num_seqs, pos0, n, cache_cap);
+  if (s != SGQA_OK) return s;
+  if ((s = check_q8(p, cache_cap)) != SGQA_OK) return s;
+  if (n == 0) return SGQA_OK;
+  REQUIRE_PTR(k, 16);
+  REQUIRE_PTR(v, 16);
+  REQUIRE_PTR(kv8, 16);
+  REQUIRE_PTR(kv_scale, 8);
+  if (pos0 % sgqa::kQ8Tok != 0 || (pos0 + n) % sgqa::kQ8Tok != 0) REQUIRE_PTR(tail, 16);
+  return do_append_q8(p, num_seqs, cache_cap, pos0, n, k, v, tail, kv8, kv_scale, static_cast<cudaStream_t>(stream));
+}
+
+sgqa_status sgqa_sparse_attn_q8(const sgqa_params* p, int64_t num_seqs, int64_t q_pos0, int64_t nq, const void* q,
+                                int64_t cache_cap, int64_t cache_len, const uint8_t* kv8, const float* kv_scale,
+                                const int32_t* sel, const int32_t* sel_count, const void* gate, int64_t* acc,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  sgqa_status s = check_common(p, num_seqs, q_pos0, nq, cache_cap);
+  if (s != SGQA_OK) return s;
+  if ((s = check_q8(p, cache_cap)) != SGQA_OK) return s;
+  if (cache_len < q_pos0 + nq || cache_len > cache_cap)
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "need q_pos0 + nq <= cache_len <= cache_cap");
+  if (nq == 0) return SGQA_OK;
+  REQUIRE_PTR(q, 16);
+  REQUIRE_PTR(kv8, 16);
+  REQUIRE_PTR(kv_scale, 8);
+  REQUIRE_PTR(sel, 4);
+  REQUIRE_PTR(sel_count, 4);
+  REQUIRE_PTR(out, 16);
+  if (gate != nullptr && !aligned(gate, 2)) return fail(SGQA_ERR_INVALID_ARGUMENT, "gate must be 2-byte aligned");
+  if (acc != nullptr && !aligned(acc, 8)) return fail(SGQA_ERR_INVALID_ARGUMENT, "acc must be 8-byte aligned");
+  if ((s = check_ws(workspace, workspace_bytes, attn_q8_ws_bytes(p, num_seqs, nq, acc != nullptr))) != SGQA_OK) return s;
+  const Q8Cache c{kv8, kv_scale, cache_cap / sgqa::kQ8Tok};
+  return do_attn_q8(p, num_seqs, q_pos0, nq, q, c, sel, sel_count, gate, acc, out, workspace,
+                    static_cast<cudaStream_t>(stream));
+}
+
+sgqa_status sgqa_forward_q8(const sgqa_params* p, int64_t num_seqs, int64_t q_pos0, int64_t nq, const void* q,
+                            const void* idx_q, const float* idx_w, int64_t cache_cap, const void* proxy_k,
+                            const void* comp_logits, const void* k, const void* v, void* tail, uint8_t* kv8,
+                            float* kv_scale, float* merged_f32, uint8_t* store, int32_t* sel, int32_t* sel_count,
+                            const void* gate, int64_t* acc, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  g_err.clear();
+  sgqa_status s = check_common(p, num_seqs, q_pos0, nq, cache_cap);
+  if (s != SGQA_OK) return s;
+  if ((s = check_q8(p, cache_cap)) != SGQA_OK) return s;
+  if (nq == 0) return SGQA_OK;
+  REQUIRE_PTR(q, 16);
+  REQUIRE_PTR(idx_q, 16);
+  REQUIRE_PTR(idx_w, 8);
+  REQUIRE_PTR(proxy_k, 16);
+  REQUIRE_PTR(comp_logits, 16);
+  REQUIRE_PTR(k, 16);
+  REQUIRE_PTR(v, 16);
+  REQUIRE_PTR(kv8, 16);
+  REQUIRE_PTR(kv_scale, 8);
+  REQUIRE_PTR(store, 16);
+  REQUIRE_PTR(sel, 4);
+  REQUIRE_PTR(sel_count, 4);
+  REQUIRE_PTR(out, 16);
+  if (q_pos0 % sgqa::kQ8Tok != 0 || (q_pos0 + nq) % sgqa::kQ8Tok != 0) REQUIRE_PTR(tail, 16);
+  if (merged_f32 != nullptr && !aligned(merged_f32, 16))
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "merged_f32 must be 16-byte aligned");
+  if (gate != nullptr && !aligned(gate, 2)) return fail(SGQA_ERR_INVALID_ARGUMENT, "gate must be 2-byte aligned");
+  if (acc != nullptr && !aligned(acc, 8)) return fail(SGQA_ERR_INVALID_ARGUMENT, "acc must be 8-byte aligned");
+  if ((s = check_ws(workspace, workspace_bytes, forward_q8_ws_bytes(p, num_seqs, nq, q_pos0 + nq))) != SGQA_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int B = p->block_size;
+  if ((s = do_merge(p, num_seqs, cache_cap, proxy_k, comp_logits, q_pos0 / B, (q_pos0 + nq) / B, merged_f32, store,
+                    st)) != SGQA_OK)
+    return s;
+  if ((s = do_append_q8(p, num_seqs, cache_cap, q_pos0, nq, k, v, tail, kv8, kv_scale, st)) != SGQA_OK) return s;
+  if ((s = do_index(p, num_seqs, q_pos0, nq, idx_q, idx_w, cache_cap, store, sel, sel_count, workspace, st)) != SGQA_OK)
+    return s;
+  const Q8Cache c{kv8, kv_scale, cache_cap / sgqa::kQ8Tok};
+  return do_attn_q8(p, num_seqs, q_pos0, nq, q, c, sel, sel_count, gate, acc, out, workspace, st);
+}
+
+sgqa_status sgqa_evict_workspace_size(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, size_t* bytes) {
+  g_err.clear();
+  sgqa_status s = check_common(p, num_seqs, 0, 0, cache_cap);
+  if (s != SGQA_OK) return s;
+  if (bytes == nullptr) return fail(SGQA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+  *bytes = evict_layout(num_seqs, cache_cap / p->block_size).bytes;
+  return SGQA_OK;
+}
+
+sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap, int64_t cache_len, int64_t keep,
+                       int64_t first, int64_t recent, const int64_t* acc, const int32_t* pos, int64_t pos_count,
+                       int64_t evicted, int64_t* acc_out, int32_t* pos_out, const sgqa_cache_array* arrays,
+                       int32_t num_arrays, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err.clear();
+  sgqa_status s = check_common(p, num_seqs, 0, 0, cache_cap);
+  if (s != SGQA_OK) return s;
+  const int B = p->block_size;
+  if (cache_cap % B != 0)
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "cache_cap (%lld) must be a multiple of block_size", (long long)cache_cap);
+  if (cache_len < 0 || cache_len > cache_cap)
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "need 0 <= cache_len <= cache_cap");
+  const int64_t n = cache_len / B, slots = cache_cap / B;
+  const int part = cache_len % B != 0;
+  if (first < 0 || recent < 0 || keep < 0 || keep > n || first > keep || recent > keep - first)
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "need first + recent <= keep <= %lld complete blocks", (long long)n);
+  if (pos_count < 0 || pos_count > n || evicted < 0 || evicted > INT32_MAX - slots)
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "need 0 <= pos_count <= complete blocks and block numbers below 2^31");
+  if (num_arrays < 0 || num_arrays > sgqa::kMaxArrays || (num_arrays > 0 && arrays == nullptr))
+    return fail(SGQA_ERR_INVALID_ARGUMENT, "arrays: at most %d", sgqa::kMaxArrays);
+  if (slots == 0) return SGQA_OK;
+  REQUIRE_PTR(acc, 8);
+  REQUIRE_PTR(acc_out, 8);
+  REQUIRE_PTR(pos_out, 4);
+  if (pos_count > 0) REQUIRE_PTR(pos, 4);
+  sgqa::EvictArrays ar{};
+  ar.count = num_arrays;
+  for (int i = 0; i < num_arrays; ++i) {
+    if (arrays[i].data == nullptr || arrays[i].block_bytes < 1)
+      return fail(SGQA_ERR_INVALID_ARGUMENT, "array %d: NULL or without bytes", i);
+    ar.base[i] = static_cast<uint8_t*>(arrays[i].data);
+    ar.bytes[i] = arrays[i].block_bytes;
+    ar.tail_only[i] = arrays[i].tail_only != 0;
+    int shift = 4;  // the widest word that address and size allow
+    while (shift > 0 && ((reinterpret_cast<uintptr_t>(arrays[i].data) | static_cast<uintptr_t>(arrays[i].block_bytes)) &
+                         ((1u << shift) - 1)))
+      --shift;
+    ar.shift[i] = shift;
+  }
+  const EvictLayout l = evict_layout(num_seqs, slots);
+  if ((s = check_ws(workspace, workspace_bytes, l.bytes)) != SGQA_OK) return s;
+  if (num_seqs > 65535) return fail(SGQA_ERR_UNSUPPORTED, "at most 65535 sequences per call");
+  sgqa::EvictWs ws;
+  ws.cap = slots;
+  ws.moves = ws_at<int2>(workspace, l.moves_off);
+  ws.moved_acc = ws_at<int64_t>(workspace, l.macc_off);
+  ws.moved_pos = ws_at<int32_t>(workspace, l.mpos_off);
+  ws.count = ws_at<int32_t>(workspace, l.count_off);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  sgqa::evict_select_kernel<<<static_cast<unsigned>(num_seqs), sgqa::kEvictThreads, 0, st>>>(
+      acc, pos, pos_count, evicted, n, part, keep, first, recent, slots, ws, acc_out, pos_out);
+  SGQA_LAUNCH_CHECK("evict_select_kernel");
+  const int64_t most = std::min(keep, n - keep) + part;  // moves of a sequence
+  if (num_arrays == 0 || keep == n || most == 0) return SGQA_OK;
+  const int64_t per_seq = std::min<int64_t>(most, std::max<int64_t>(1, 8 * kSmCount / num_seqs));
+  sgqa::evict_move_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(num_seqs)), 256, 0, st>>>(
+      ar, ws, n, part, keep, slots);
+  SGQA_LAUNCH_CHECK("evict_move_kernel");
+  return SGQA_OK;
 }
 
 sgqa_status sgqa_set_wait_limit_ns(uint64_t ns) {

@@ -63,7 +63,8 @@ class Params:
     scale: float = 0.0
 
     def c(self) -> _Params:
-        return _Params(*dataclasses.astuple(self))
+        return _Params(self.num_kv_groups, self.heads_per_group, self.head_dim, self.idx_heads, self.idx_dim,
+                       self.block_size, self.topk, self.merge_in_f32, self.scale)
 
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
@@ -216,29 +217,83 @@ def alloc_workspace_q8(p: Params, num_seqs: int, nq: int, max_ctx: int, device) 
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
+def _check(name, t, dtype, numel, exact=True):
+    """Address of a contiguous CUDA tensor that holds what the call reads or writes there."""
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or (t.numel() != numel if exact else t.numel() < numel):
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {numel} {dtype} values, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _run(fn, lead, stream, *args):
+    """Call fn on the tensors' own device, on the given stream or that device's current one."""
+    dev = lead.device
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    if dev.index == torch.cuda.current_device():
+        _ok(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _ok(fn(*args, stream.cuda_stream))
+
+
+def _q8_cache(p, S, cap, kv8, kv_scale):
+    n = S * cap // 8 * p.num_kv_groups * 2
+    return _check("kv8", kv8, torch.uint8, n * 8 * p.head_dim), _check("kv_scale", kv_scale, torch.float32, n)
+
+
+def _workspace(ws):
+    if ws is None:
+        return None, 0
+    return _check("workspace", ws, torch.uint8, 0, exact=False), ws.numel()
+
+
 def sgqa_kv_append_q8(p: Params, num_seqs, cache_cap, pos0, n, k, v, tail, kv8, kv_scale, stream=None):
     """Quantise the K/V rows of positions [pos0, pos0 + n) (k, v: [S, n, G, D] bf16) into the 8-bit cache."""
-    _ok(_lib.sgqa_kv_append_q8(ctypes.byref(p.c()), num_seqs, cache_cap, pos0, n, _ptr(k), _ptr(v), _ptr(tail),
-                               _ptr(kv8), _ptr(kv_scale), _stream(stream)))
+    row = num_seqs * p.num_kv_groups * p.head_dim
+    _run(_lib.sgqa_kv_append_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, cache_cap, pos0, n,
+         _check("k", k, torch.bfloat16, row * n), _check("v", v, torch.bfloat16, row * n),
+         None if tail is None else _check("tail", tail, torch.bfloat16, row * 16),
+         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale))
 
 
 def sgqa_sparse_attn_q8(p: Params, num_seqs, q_pos0, nq, q, cache_cap, cache_len, kv8, kv_scale, sel, sel_count, out,
                         workspace=None, gate=None, acc=None, stream=None):
     """Attention over the 8-bit cache; acc ([S, cache_cap / 8] int64, units of 2^-32) gains the blocks' weights."""
-    _ok(_lib.sgqa_sparse_attn_q8(ctypes.byref(p.c()), num_seqs, q_pos0, nq, _ptr(q), cache_cap, cache_len, _ptr(kv8),
-                                 _ptr(kv_scale), _ptr(sel), _ptr(sel_count), _ptr(gate), _ptr(acc), _ptr(out),
-                                 _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                                 _stream(stream)))
+    rows = num_seqs * nq * p.num_kv_groups
+    heads = rows * p.heads_per_group
+    _run(_lib.sgqa_sparse_attn_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, q_pos0, nq,
+         _check("q", q, torch.bfloat16, heads * p.head_dim), cache_cap, cache_len,
+         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale), _check("sel", sel, torch.int32, rows * p.topk),
+         _check("sel_count", sel_count, torch.int32, rows),
+         None if gate is None else _check("gate", gate, torch.bfloat16, heads),
+         None if acc is None else _check("acc", acc, torch.int64, num_seqs * cache_cap // 8),
+         _check("out", out, torch.bfloat16, heads * p.head_dim), *_workspace(workspace))
 
 
 def sgqa_forward_q8(p: Params, num_seqs, q_pos0, nq, q, idx_q, idx_w, cache_cap, proxy_k, comp_logits, k, v, tail, kv8,
                     kv_scale, merged_f32, store, sel, sel_count, out, workspace, gate=None, acc=None, stream=None):
     """merge -> append (k, v: the call's own rows) -> index/top-k -> attention over the 8-bit cache."""
-    _ok(_lib.sgqa_forward_q8(ctypes.byref(p.c()), num_seqs, q_pos0, nq, _ptr(q), _ptr(idx_q), _ptr(idx_w), cache_cap,
-                             _ptr(proxy_k), _ptr(comp_logits), _ptr(k), _ptr(v), _ptr(tail), _ptr(kv8), _ptr(kv_scale),
-                             _ptr(merged_f32), _ptr(store), _ptr(sel), _ptr(sel_count), _ptr(gate), _ptr(acc),
-                             _ptr(out), _ptr(workspace), workspace.numel() if workspace is not None else 0,
-                             _stream(stream)))
+    rows = num_seqs * nq * p.num_kv_groups
+    heads, blocks = rows * p.heads_per_group, num_seqs * cache_cap // 8
+    in_dt = torch.float32 if p.merge_in_f32 else torch.bfloat16
+    kv, sc = _q8_cache(p, num_seqs, cache_cap, kv8, kv_scale)
+    _run(_lib.sgqa_forward_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, q_pos0, nq,
+         _check("q", q, torch.bfloat16, heads * p.head_dim),
+         _check("idx_q", idx_q, torch.bfloat16, rows * p.idx_heads * p.idx_dim),
+         _check("idx_w", idx_w, torch.float32, rows * p.idx_heads), cache_cap,
+         _check("proxy_k", proxy_k, in_dt, num_seqs * cache_cap * p.idx_dim),
+         _check("comp_logits", comp_logits, in_dt, num_seqs * cache_cap * p.idx_dim),
+         _check("k", k, torch.bfloat16, rows * p.head_dim), _check("v", v, torch.bfloat16, rows * p.head_dim),
+         None if tail is None else _check("tail", tail, torch.bfloat16, num_seqs * 16 * p.num_kv_groups * p.head_dim),
+         kv, sc, None if merged_f32 is None else _check("merged_f32", merged_f32, torch.float32, blocks * p.idx_dim),
+         _check("store", store, torch.uint8, blocks * p.idx_dim), _check("sel", sel, torch.int32, rows * p.topk),
+         _check("sel_count", sel_count, torch.int32, rows),
+         None if gate is None else _check("gate", gate, torch.bfloat16, heads),
+         None if acc is None else _check("acc", acc, torch.int64, blocks),
+         _check("out", out, torch.bfloat16, heads * p.head_dim), *_workspace(workspace))
 
 
 def sgqa_evict_workspace_size(p: Params, num_seqs: int, cache_cap: int) -> int:
@@ -256,15 +311,18 @@ def sgqa_evict(p: Params, num_seqs, cache_cap, cache_len, keep, first, recent, a
     """Keep the `keep` heaviest blocks of every sequence.  arrays: contiguous tensors whose leading dimensions are
     (sequence, block) or (sequence, token); tail_arrays: the same, of which only the incomplete block moves."""
     blocks = num_seqs * (cache_cap // p.block_size)
-    every = [(t, 0) for t in arrays] + [(t, 1) for t in tail_arrays]
-    for t, _ in every:
-        if not t.is_contiguous() or blocks == 0 or t.numel() * t.element_size() % blocks:
-            raise ValueError("evict: every array is contiguous and holds cache_cap / block_size blocks per sequence")
-    c = (_CacheArray * max(1, len(every)))(*[_CacheArray(t.data_ptr(), t.numel() * t.element_size() // blocks, f)
-                                             for t, f in every])
-    _ok(_lib.sgqa_evict(ctypes.byref(p.c()), num_seqs, cache_cap, cache_len, keep, first, recent, _ptr(acc), _ptr(pos),
-                        pos_count, evicted, _ptr(acc_out), _ptr(pos_out), c, len(every), _ptr(workspace),
-                        workspace.numel() if workspace is not None else 0, _stream(stream)))
+    every = []
+    for group, tail in ((arrays, 0), (tail_arrays, 1)):
+        for t in group:
+            size = t.numel() * t.element_size()
+            if not t.is_cuda or not t.is_contiguous() or blocks == 0 or size % blocks:
+                raise ValueError("evict: every array is a contiguous CUDA tensor of cache_cap / block_size blocks per sequence")
+            every.append(_CacheArray(t.data_ptr(), size // blocks, tail))
+    c = (_CacheArray * max(1, len(every)))(*every)
+    _run(_lib.sgqa_evict, acc, stream, ctypes.byref(p.c()), num_seqs, cache_cap, cache_len, keep, first, recent,
+         _check("acc", acc, torch.int64, blocks), None if pos is None else _check("pos", pos, torch.int32, blocks),
+         pos_count, evicted, _check("acc_out", acc_out, torch.int64, blocks), _check("pos_out", pos_out, torch.int32, blocks),
+         c, len(every), *_workspace(workspace))
 
 
 def sgqa_set_wait_limit_ns(ns: int):

@@ -1,0 +1,527 @@
+// Sparse attention over the 8-bit K/V cache (layout: kv8.cuh) on the tcgen05
+// tensor cores, which take the E4M3 codes as they lie: nothing is widened.
+//
+// A query and a softmax weight are not rounded to 8 bits.  Each is split into
+// two E4M3 values, x = hi + lo / 16 with hi = E4M3(x), lo = E4M3(16 (x - hi)):
+// a BF16 query value (8 significant bits) is carried exactly over 2^13 of
+// range below the row's largest, a weight to 2^-8 of itself.  The two halves
+// are MMA columns (or MMA steps) side by side, so K or V is read once for
+// both.  With one scale per (block, group), a block's K scale multiplies its
+// scores and its V scale its weights.
+//
+// Softmax reference.  The weights that enter the MMA are 2^(s + log2 vs - ref):
+// the reference follows the scores plus the logarithm of the V scale, so that
+// blocks of small values keep their bits where they carry the result.  The sum
+// of the weights, FP32, uses the same reference without the V scale.
+#pragma once
+#include <cooperative_groups.h>
+
+#include "kv8.cuh"
+#include "tc.cuh"
+
+namespace sgqa {
+
+// Byte offset of byte c (0..63) of row r in tiles of 64-byte rows (512-byte atoms).
+__device__ __forceinline__ uint32_t sw64_offset(uint32_t r, uint32_t c) {
+  const uint32_t a = r * 64u + c;
+  return a ^ (((a >> 7) & 3u) << 4);
+}
+
+// Exponent e of the smallest power of two with amax / 2^e <= 448 (amax > 0
+// finite or zero; at least kQ8MinExp).
+__device__ __forceinline__ int e4m3_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  return max(static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), kQ8MinExp);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+// hi and 16 x lo codes of two values (low 16 bits each).
+__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo, float lo_scale) {
+  hi = e4m3x2(a, b);
+  const float2 h = e4m3x2_value(hi);
+  lo = e4m3x2((a - h.x) * lo_scale, (b - h.y) * lo_scale);
+}
+
+// ---------------------------------------------------------------------------
+// Few queries (decode): an HBM-bound gather.  One CTA takes a range of one
+// (query, group)'s blocks (split-K), 16 blocks = 128 tokens at a time, and
+// computes transposed, so that the 16 heads are the narrow MMA side:
+//   S^T [128 tokens x 32] = K [128 x 192] Q^T     6 MMAs (M128 N32 K32): columns
+//                           16 heads' hi | 16 heads' lo; K as gathered (K-major)
+//   softmax               one thread per token, 16 heads in registers
+//   O^T [192 dims x 32] += V^T [192 x 128] P^T    2 x 4 MMAs (M128 N32 K32): V as
+//                           gathered (MN-major), dims 0-127 and 64-191 (the rows
+//                           computed twice are not read); P through shared memory
+// A token's max over heads never crosses threads: the reference moves only when
+// some weight exceeds 2^8 (one barrier-or per tile tells), and only then are
+// the 16 maxima reduced over the tile and O rescaled in TMEM.
+// One box (3 KB: a block's K and V) per block, issued by 16 lanes side by
+// side; K and V share a stage.  The splits of a row form one cluster and
+// combine through distributed shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kQdTile = 16;       // blocks per tile
+constexpr int kQdStages = 2;
+constexpr int kQdThreads = 224;   // producer, QK issuer, 4 softmax warps, PV issuer
+constexpr int kQdCols = 128;      // TMEM: S 2 x 32, O 2 x 32
+constexpr int kQdMaxSplit = 8;    // splits of a row = one (portable) cluster
+
+struct __align__(1024) QdSmem {
+  uint8_t kv[kQdStages][kQdTile][3][16][64];  // [block][chunk of 64 dims][8 K rows, 8 V rows][64 B], 64-byte swizzle
+  uint8_t q[3][32][64];                       // [chunk][16 hi, 16 lo][64 B], 64-byte swizzle
+  uint8_t p[2][kQdTile * kQ8Tok][32];         // [token][16 hi, 16 lo], 32-byte swizzle
+  float2 scale[kQdStages][kQdTile];           // K and V scale of a stage's blocks
+  uint32_t mask[kQdStages][kQdTile];          // their attended tokens
+  float wmax[4][kHg];                         // a reference change: maxima of the four warps
+  float qscale[kHg];
+  uint64_t full[kQdStages], empty[kQdStages], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, o_final, drain[2];
+  uint32_t tmem;
+  int abort;
+};
+
+// The combine's view of the ring, once the last MMA is done.
+struct QdOut {
+  float m[kHg], l[kHg];            // this split's reference and sum
+  float f[kQdMaxSplit][kHg];       // factor of every split
+  float fin[kHg], wfac[kHg];       // normalisation (and gate); weight normalisation
+  float wl[4][kHg];
+  float o[kHg][kD + 1];
+};
+
+// Workspace of the weights: per (row, block of the row) 16 heads' sums, then per
+// (row, tile) the references they refer to.
+struct QdWeights {
+  int64_t* acc;   // nullptr: not wanted
+  float* sums;    // [rows, k + 1, 16]
+  float* refs;    // [rows, tiles, 16]
+  int tiles;      // per row (nsplit x tiles of a split)
+};
+
+template <bool WEIGHTS>
+__global__ void __launch_bounds__(kQdThreads, 2)
+attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfloat16* __restrict__ q,
+                      const float* __restrict__ kv_scale, const int32_t* __restrict__ sel,
+                      const int32_t* __restrict__ sel_count, const __nv_bfloat16* __restrict__ gate,
+                      __nv_bfloat16* __restrict__ out, QdWeights wts, int64_t nq, int G, int k, int64_t q_pos0,
+                      int64_t blocks, int nsplit, float scale_log2) {
+  extern __shared__ uint8_t smem_raw[];
+  QdSmem& sm = *reinterpret_cast<QdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % nsplit;
+  const int64_t row = blockIdx.x / nsplit;  // (seq * nq + i) * G + g
+  const int g = static_cast<int>(row % G);
+  const int64_t i = (row / G) % nq;
+  const int64_t seq = row / (G * nq);
+  const int64_t t = q_pos0 + i, hist = t / kQ8Tok;
+  const int cnt = min(max(sel_count[row], 0), k);
+  const int32_t* ids = sel + row * k;
+  const int nblk = cnt + 1;  // selected blocks, then the current block
+  const int per = (nblk + nsplit - 1) / nsplit;
+  const int b0 = min(nblk, split * per), b1 = min(nblk, b0 + per);
+  const int n_tiles = (b1 - b0 + kQdTile - 1) / kQdTile;
+  volatile int* abort = &sm.abort;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int s = 0; s < kQdStages; ++s) {
+      tc::mbar_init(bar(sm.full[s]), kQdTile);
+      tc::mbar_init(bar(sm.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(bar(sm.s_full[b]), 1);
+      tc::mbar_init(bar(sm.s_free[b]), 128);
+      tc::mbar_init(bar(sm.p_full[b]), 128);
+      tc::mbar_init(bar(sm.pv_done[b]), 1);
+      tc::mbar_init(bar(sm.drain[b]), 1);
+    }
+    tc::mbar_init(bar(sm.q_full), 128);
+    tc::mbar_init(bar(sm.o_final), 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == 1) tc::tmem_alloc(smem_u32(&sm.tmem), kQdCols);
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tS = sm.tmem, tO = sm.tmem + 64;
+  int issued = 0;  // producer: tiles whose copies this warp issued
+
+  // per-head state of the softmax threads
+  float ref[kHg], l[kHg];
+#pragma unroll
+  for (int h = 0; h < kHg; ++h) { ref[h] = -INFINITY; l[h] = 0.f; }
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) tc::prefetch_tmap(&kvmap);
+    // block of position b (-1: none): ids and their predecessors are fetched
+    // two tiles ahead, the scales one
+    auto fetch = [&](int j, int& id, int& prev) {
+      const int b = b0 + j * kQdTile + lane;
+      id = prev = -1;
+      if (lane < kQdTile && b < b1 && b < cnt) {
+        id = __ldg(ids + b);
+        if (b > 0) prev = __ldg(ids + b - 1);
+      }
+    };
+    auto resolve = [&](int j, int id, int prev) -> int32_t {
+      const int b = b0 + j * kQdTile + lane;
+      if (lane >= kQdTile || b >= b1) return -1;
+      if (b == cnt) return static_cast<int32_t>(hist);
+      if (id < 0 || id >= hist || id <= prev) {
+        report(kDevBounds);
+        return -1;
+      }
+      return id;
+    };
+    auto scales = [&](int32_t blk) -> float2 {
+      return blk >= 0 ? __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g) : make_float2(0.f, 1.f);
+    };
+    int id1, prev1, id2, prev2;
+    fetch(0, id1, prev1);
+    fetch(1, id2, prev2);
+    int32_t blk = resolve(0, id1, prev1);
+    float2 sc = scales(blk);
+    for (int j = 0; j < n_tiles; ++j) {
+      const int s = j % kQdStages;
+      if (j >= kQdStages && !tc::warp_wait(bar(sm.empty[s]), ((j / kQdStages) - 1) & 1, abort)) break;
+      if (lane < kQdTile) {
+        const uint32_t full = bar(sm.full[s]);
+        tc::mbar_expect_only(full, kQ8Blk);
+        // no block: a box outside the cache, filled with zeros
+        tc::tma_load_5d(smem_u32(&sm.kv[s][lane][0][0][0]), &kvmap, 0, 0, 0, blk >= 0 ? g : 0,
+                        blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
+        sm.scale[s][lane] = sc;
+        sm.mask[s][lane] = blk < 0 ? 0u : blk == hist ? (2u << (t % kQ8Tok)) - 1u : 0xFFu;
+        tc::mbar_arrive(full);
+      }
+      __syncwarp();
+      issued = j + 1;
+      blk = resolve(j + 1, id2, prev2);
+      sc = scales(blk);
+      fetch(j + 2, id2, prev2);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S^T = K Q^T
+    const uint32_t id_qk = tc::idesc_e4m3(128, 32, false, false);
+    const uint64_t dk0 = tc::sdesc(smem_u32(&sm.kv[0][0][0][0][0]), 16, kQ8Blk, tc::kSw64);
+    const uint64_t dq0 = tc::sdesc(smem_u32(&sm.q[0][0][0]), 16, 512, tc::kSw64);
+    bool ok = tc::warp_wait(bar(sm.q_full), 0, abort);
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      const int s = j % kQdStages, b = j & 1;
+      ok = tc::warp_wait(bar(sm.full[s]), (j / kQdStages) & 1, abort);
+      if (ok && j >= 2) ok = tc::warp_wait(bar(sm.s_free[b]), ((j >> 1) - 1) & 1, abort);
+      if (!ok) break;
+      tc::fence_after();
+      if (tc::elect_one()) {
+        const uint64_t dk = dk0 + (kQdTile * kQ8Blk / 16) * s;
+#pragma unroll
+        for (int kk = 0; kk < 6; ++kk)  // K: +1 KB per 64 dims; Q: +2 KB; both +32 B per 32 dims
+          tc::mma_f8(tS + 32 * b, dk + (kk >> 1) * 64 + (kk & 1) * 2, dq0 + (kk >> 1) * 128 + (kk & 1) * 2, id_qk,
+                     kk > 0 ? 1u : 0u);
+        tc::mma_commit(bar(sm.s_full[b]));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 6) {
+    // ---------------------------------------------------------------- O^T += V^T P^T
+    const uint32_t id_pv = tc::idesc_e4m3(128, 32, true, true);
+    // V: 64-dim chunks 1 KB apart, 8-token groups one block apart; P: 8-token groups 256 B apart
+    const uint64_t dv0 = tc::sdesc(smem_u32(&sm.kv[0][0][0][8][0]), 1024, kQ8Blk, tc::kSw64);
+    const uint64_t dp0 = tc::sdesc(smem_u32(&sm.p[0][0][0]), 256, 256, tc::kSw32);
+    bool ok = true;
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      const int s = j % kQdStages, b = j & 1;
+      ok = tc::warp_wait(bar(sm.p_full[b]), (j >> 1) & 1, abort);
+      if (!ok) break;
+      tc::fence_after();
+      if (tc::elect_one()) {
+        const uint64_t dv = dv0 + (kQdTile * kQ8Blk / 16) * s;
+        const uint64_t dp = dp0 + (kQdTile * kQ8Tok * 32 / 16) * b;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {  // 32 tokens: V +4 blocks, P +1 KB
+          const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
+          tc::mma_f8(tO, dv + kk * (4 * kQ8Blk / 16), dp + kk * 64, id_pv, acc);
+          tc::mma_f8(tO + 32, dv + 64 + kk * (4 * kQ8Blk / 16), dp + kk * 64, id_pv, acc);
+        }
+        tc::mma_commit(bar(sm.empty[s]));
+        tc::mma_commit(bar(sm.pv_done[b]));
+        if (j + 1 == n_tiles) tc::mma_commit(bar(sm.o_final));
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int sw = warp - 2, quad = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int tok = quad * 32 + lane;  // token of the tile = TMEM lane
+    // queries: a warp packs four heads, a lane dims 2 lane, 2 lane + 1 of every chunk
+#pragma unroll
+    for (int hh = 0; hh < 4; ++hh) {
+      const int h = 4 * sw + hh;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(q + (row * kHg + h) * kD);
+      float x[3][2], mx = 0.f;
+      bool fin = true;
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        const uint32_t w = src[32 * c + lane];
+        x[c][0] = __uint_as_float(w << 16);
+        x[c][1] = __uint_as_float(w & 0xFFFF0000u);
+        fin = fin && isfinite(x[c][0]) && isfinite(x[c][1]);
+        mx = fmaxf(mx, fmaxf(fabsf(x[c][0]), fabsf(x[c][1])));
+      }
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      fin = __all_sync(0xffffffffu, fin);
+      const int e = fin ? e4m3_exp(mx) : 0;
+      const float inv = pow2f(-e);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        uint32_t hi, lo;
+        split_e4m3(x[c][0] * inv, x[c][1] * inv, hi, lo, 16.f);
+        *reinterpret_cast<uint16_t*>(&sm.q[c][0][0] + sw64_offset(h, 2 * lane)) = static_cast<uint16_t>(hi);
+        *reinterpret_cast<uint16_t*>(&sm.q[c][0][0] + sw64_offset(16 + h, 2 * lane)) = static_cast<uint16_t>(lo);
+      }
+      // a query with an infinity or NaN: every score NaN
+      if (lane == 0) sm.qscale[h] = fin ? pow2f(e) * scale_log2 : __uint_as_float(0x7FC00000u);
+    }
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive(bar(sm.q_full));
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    float rc[kHg];
+#pragma unroll
+    for (int h = 0; h < kHg; ++h) rc[h] = sm.qscale[h];
+    bool ok = true;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int s = j % kQdStages, b = j & 1;
+      ok = ok && tc::mbar_wait(bar(sm.full[s]), (j / kQdStages) & 1, abort);
+      const float2 sc = sm.scale[s][tok >> 3];
+      const bool use = (sm.mask[s][tok >> 3] >> (tok & 7)) & 1u;
+      const float lvs = use ? log2f(sc.y) : 0.f;
+      ok = ok && tc::mbar_wait(bar(sm.s_full[b]), (j >> 1) & 1, abort);
+      tc::fence_after();
+      uint32_t sr[32];
+      tc::tmem_ld32(tS + 32 * b + lane_off, sr);
+      tc::tmem_ld_wait();
+      tc::fence_before();
+      tc::mbar_arrive(bar(sm.s_free[b]));
+      float x[kHg];
+      bool grow = false;
+#pragma unroll
+      for (int h = 0; h < kHg; ++h) {
+        const float v = fmaf(__uint_as_float(sr[16 + h]), 0.0625f, __uint_as_float(sr[h])) * (sc.x * rc[h]);
+        x[h] = use ? v : -INFINITY;
+        grow = grow || x[h] + lvs > ref[h] + 8.f;
+      }
+      // does any weight of the tile exceed 2^8?
+      int any;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
+          : "=r"(any)
+          : "r"(static_cast<int>(grow))
+          : "memory");
+      if (any) {
+        // new references: the largest score (plus log2 of its V scale) - 4, so that
+        // weights stay between 2^4 and 2^8 at most
+#pragma unroll
+        for (int h = 0; h < kHg; ++h) {
+          const int v = __float_as_int(fmaxf(x[h] + lvs, -INFINITY));
+          const int mx = __reduce_max_sync(0xffffffffu, v ^ ((v >> 31) & 0x7FFFFFFF));
+          if (lane == 0) sm.wmax[sw][h] = __int_as_float(mx ^ ((mx >> 31) & 0x7FFFFFFF));
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        float al[kHg];
+#pragma unroll
+        for (int h = 0; h < kHg; ++h) {
+          const float mx = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h]));
+          const float nr = mx > ref[h] + 8.f ? mx - 4.f : ref[h];
+          al[h] = nr == ref[h] ? 1.f : exp2f(ref[h] - nr);
+          ref[h] = nr;
+          l[h] *= al[h];
+        }
+        if (j > 0) {  // O holds P(j-1) V(j-1) by then
+          ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, abort);
+          tc::fence_after();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + 32 * half + lane_off, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * al[h & 15]);
+            tc::tmem_st32(tO + 32 * half + lane_off, o);
+          }
+          tc::tmem_st_wait();
+        }
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int h = 0; h < kHg; h += 2) {
+        float pl[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float r = ref[h + e] == -INFINITY ? 0.f : ref[h + e];
+          pl[e] = fast_exp2(x[h + e] - r);
+          l[h + e] += pl[e];
+          x[h + e] = pl[e];
+        }
+        uint32_t a, c;
+        const float vs = use ? sc.y : 0.f;
+        split_e4m3(pl[0] * vs, pl[1] * vs, a, c, 16.f);
+        if (h & 2) {
+          hi[h >> 2] |= a << 16;
+          lo[h >> 2] |= c << 16;
+        } else {
+          hi[h >> 2] = a;
+          lo[h >> 2] = c;
+        }
+      }
+      // P buffer b is free once O += P(j-2) V(j-2) has read it
+      if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j >> 1) - 1) & 1, abort);
+      {
+        uint8_t* pr = &sm.p[b][tok][0];
+        const uint32_t sw = ((tok >> 2) & 1) << 4;
+        *reinterpret_cast<uint4*>(pr + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(pr + (16 ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      tc::fence_proxy_async_smem();
+      tc::fence_before();
+      tc::mbar_arrive(bar(sm.p_full[b]));
+      if (WEIGHTS) {
+        // sums over the block's eight tokens (lanes): every exchange halves the
+        // heads a lane holds; lane r of a block ends with heads 2 r, 2 r + 1
+        float y[8], z[4], w2[2];
+        const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] = (h4 ? x[8 + c] : x[c]) + __shfl_xor_sync(0xffffffffu, h4 ? x[c] : x[8 + c], 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) z[c] = (h2 ? y[4 + c] : y[c]) + __shfl_xor_sync(0xffffffffu, h2 ? y[c] : y[4 + c], 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) w2[c] = (h1 ? z[2 + c] : z[c]) + __shfl_xor_sync(0xffffffffu, h1 ? z[c] : z[2 + c], 1);
+        const int blk = b0 + j * kQdTile + (tok >> 3);
+        if (blk < b1)
+          *reinterpret_cast<float2*>(wts.sums + (row * (k + 1) + blk) * kHg + 2 * (lane & 7)) = make_float2(w2[0], w2[1]);
+        if (tok == 0) {
+          float* r = wts.refs + (row * wts.tiles + split * (wts.tiles / nsplit) + j) * kHg;
+#pragma unroll
+          for (int h = 0; h < kHg; ++h) r[h] = ref[h];
+        }
+      }
+    }
+    if (n_tiles > 0) ok = ok && tc::mbar_wait(bar(sm.o_final), 0, abort);
+  }
+  // Every role has left its loop, so the abort flag is final; on the failure
+  // path the copies and MMAs in flight land before their memory is reused.
+  __syncthreads();
+  if (sm.abort) {
+    if (warp == 0) {
+      for (int j = max(issued - kQdStages, 0); j < issued; ++j) tc::mbar_drain(bar(sm.full[j % kQdStages]), (j / kQdStages) & 1);
+    } else if (warp == 1 || warp == 6) {
+      uint64_t& d = sm.drain[warp == 1 ? 0 : 1];
+      if (tc::elect_one()) tc::mma_commit(bar(d));
+      __syncwarp();
+      tc::mbar_drain(bar(d), 0);
+    }
+  }
+  __syncthreads();
+  QdOut& po = *reinterpret_cast<QdOut*>(&sm.kv[0][0][0][0][0]);
+  if (warp >= 2 && warp <= 5) {
+    const int quad = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    if (n_tiles > 0) {
+      tc::fence_after();
+      const int d = quad * 32 + lane;
+      uint32_t o[32];
+      tc::tmem_ld32(tO + lane_off, o);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int h = 0; h < kHg; ++h) po.o[h][d] = fmaf(__uint_as_float(o[16 + h]), 0.0625f, __uint_as_float(o[h]));
+      if (quad >= 2) {
+        tc::tmem_ld32(tO + 32 + lane_off, o);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < kHg; ++h) po.o[h][64 + d] = fmaf(__uint_as_float(o[16 + h]), 0.0625f, __uint_as_float(o[h]));
+      }
+    } else {
+      for (int x = threadIdx.x - 64; x < kHg * (kD + 1); x += 128) (&po.o[0][0])[x] = 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < kHg; ++h) {
+      float v = l[h];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) po.wl[warp - 2][h] = v;
+      if (warp == 2 && lane == 0) po.m[h] = ref[h];
+    }
+    tc::fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::tmem_dealloc(sm.tmem, kQdCols);
+  }
+  if (threadIdx.x < kHg) po.l[threadIdx.x] = (po.wl[0][threadIdx.x] + po.wl[1][threadIdx.x]) + (po.wl[2][threadIdx.x] + po.wl[3][threadIdx.x]);
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  if (threadIdx.x < kHg) {
+    const int h = threadIdx.x;
+    float mm = -INFINITY;
+    for (int r = 0; r < nsplit; ++r) mm = fmaxf(mm, cluster.map_shared_rank(po.m, r)[h]);
+    const float mu = mm == -INFINITY ? 0.f : mm;
+    float ls = 0.f;
+    for (int r = 0; r < nsplit; ++r) {
+      const float lr = cluster.map_shared_rank(po.l, r)[h];
+      const float a = exp2f(cluster.map_shared_rank(po.m, r)[h] - mu);
+      po.f[r][h] = a;
+      ls += lr == 0.f ? 0.f : a * lr;
+    }
+    po.fin[h] = gate_factor(gate, row * kHg + h) / ls;
+    // a weight sum with reference r counts 2^(r - mu) / ls
+    if (WEIGHTS) po.wfac[h] = 1.f / ls;
+  }
+  __syncthreads();
+  {
+    // this split finalises outputs [split * n, split * n + n) of the row's 16 x 192
+    const int n = (kHg * kD + nsplit - 1) / nsplit;
+    const int i0 = split * n, i1 = min(kHg * kD, i0 + n);
+    for (int x = i0 + threadIdx.x; x < i1; x += kQdThreads) {
+      const int h = x / kD, d = x - h * kD;
+      float a = 0.f;
+      for (int r = 0; r < nsplit; ++r) a = fmaf(po.f[r][h], cluster.map_shared_rank(&po.o[0][0], r)[h * (kD + 1) + d], a);
+      out[row * kHg * kD + x] = __float2bfloat16_rn(a * po.fin[h]);
+    }
+  }
+  if (WEIGHTS) {
+    // the common reference (largest of the splits')
+    float mu[kHg];
+    if (static_cast<int>(threadIdx.x) < b1 - b0) {
+#pragma unroll
+      for (int h = 0; h < kHg; ++h) {
+        float mm = -INFINITY;
+        for (int r = 0; r < nsplit; ++r) mm = fmaxf(mm, cluster.map_shared_rank(po.m, r)[h]);
+        mu[h] = mm == -INFINITY ? 0.f : mm;
+      }
+    }
+    for (int x = threadIdx.x; x < b1 - b0; x += kQdThreads) {
+      const int b = b0 + x;
+      const int64_t blk = b == cnt ? hist : ids[b];
+      if (blk < 0 || blk > hist || (b < cnt && (blk == hist || (b > 0 && blk <= ids[b - 1])))) continue;  // reported
+      const float* ws = wts.sums + (row * (k + 1) + b) * kHg;
+      const float* rs = wts.refs + (row * wts.tiles + split * (wts.tiles / nsplit) + x / kQdTile) * kHg;
+      float w = 0.f;
+#pragma unroll
+      for (int h = 0; h < kHg; ++h) {
+        const float v = ws[h];
+        w += v == 0.f ? 0.f : v * exp2f((rs[h] == -INFINITY ? 0.f : rs[h]) - mu[h]) * po.wfac[h];
+      }
+      acc_add(wts.acc + seq * blocks + blk, w);
+    }
+  }
+  cluster.sync();  // no split leaves while others still read its shared memory
+}
+
+}  // namespace sgqa

@@ -15,6 +15,7 @@
 
 #include "../../include/sgqa.h"
 #include "attn_mma.cuh"
+#include "attn_q8.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
 #include "evict.cuh"
@@ -656,8 +657,47 @@ sgqa_status do_append_q8(const sgqa_params* p, int64_t S, int64_t cap, int64_t p
   return SGQA_OK;
 }
 
+// Splits of a row in the decode kernel: one wave of two CTAs per SM, at most a
+// portable cluster, and no split without a tile of its own.
+int q8_splits(const sgqa_params* p, int64_t rows, int64_t max_ctx) {
+  const int64_t most = std::min<int64_t>(p->topk, (max_ctx - 1) / sgqa::kQ8Tok) + 1;  // blocks of a row
+  const int64_t tiles = (most + sgqa::kQdTile - 1) / sgqa::kQdTile;
+  return static_cast<int>(std::min<int64_t>({decode_splits(rows), sgqa::kQdMaxSplit, tiles}));
+}
+
+struct Q8Ws {
+  size_t sums_off, refs_off, bytes;
+};
+Q8Ws attn_q8_ws(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
+  Q8Ws w{};
+  const size_t rows = static_cast<size_t>(S * nq * p->num_kv_groups);
+  if (nq <= kDecodeMaxNq) {
+    if (!weights) return w;
+    // at most one more tile per split than the row's blocks fill
+    const size_t tiles = static_cast<size_t>(p->topk + 1) / sgqa::kQdTile + 1 + sgqa::kQdMaxSplit;
+    w.refs_off = align256(rows * static_cast<size_t>(p->topk + 1) * sgqa::kHg * 4);
+    w.bytes = w.refs_off + align256(rows * tiles * sgqa::kHg * 4);
+    return w;
+  }
+  return w;
+}
 size_t attn_q8_ws_bytes(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
-  return 0;
+  return attn_q8_ws(p, S, nq, weights).bytes;
+}
+
+// Tensor map of the cache as (64 codes, rows of K then V, chunk of 64 dims, group, block).
+sgqa_status q8_map(const Q8Cache& c, int G, int64_t S, int rows, CUtensorMap* m) {
+  auto enc = tmap_encoder();
+  if (enc == nullptr) return fail(SGQA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[5] = {64, 2 * sgqa::kQ8Tok, 3, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(S * c.blocks)};
+  cuuint64_t strides[4] = {sgqa::kD, 64, sgqa::kQ8Blk, static_cast<cuuint64_t>(G) * sgqa::kQ8Blk};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), 3, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(c.kv8), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SGQA_ERR_CUDA, "tensor map for kv8: CUresult %d", (int)r);
+  return SGQA_OK;
 }
 
 // Workspace of sgqa_forward_q8 (its steps run in turn).
@@ -669,13 +709,51 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
                        const int32_t* sel, const int32_t* sel_count, const void* gate, int64_t* acc, void* out, void* ws,
                        cudaStream_t st) {
   const int64_t rows = S * nq * p->num_kv_groups;
-  if (rows > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "too many queries for one call");
+  if (rows > INT32_MAX / sgqa::kQdMaxSplit) return fail(SGQA_ERR_UNSUPPORTED, "too many queries for one call");
+  if (S * c.blocks > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "cache of 2^31 blocks or more");
+  const float scale_log2 = softmax_scale(p) * 1.4426950408889634f;
+  const Q8Ws w = attn_q8_ws(p, S, nq, acc != nullptr);
+  if (nq <= kDecodeMaxNq) {
+    CUtensorMap m;
+    sgqa_status s = q8_map(c, p->num_kv_groups, S, 2 * sgqa::kQ8Tok, &m);
+    if (s != SGQA_OK) return s;
+    const int nsplit = q8_splits(p, rows, q0 + nq);
+    const int per = (std::min<int>(p->topk, static_cast<int>(std::min<int64_t>((q0 + nq - 1) / sgqa::kQ8Tok, p->topk))) + nsplit) / nsplit;
+    sgqa::QdWeights wt{};
+    if (acc != nullptr) {
+      wt.acc = acc;
+      wt.sums = ws_at<float>(ws, w.sums_off);
+      wt.refs = ws_at<float>(ws, w.refs_off);
+      wt.tiles = nsplit * ((per + sgqa::kQdTile - 1) / sgqa::kQdTile);
+    }
+    static_assert(2 * (sizeof(sgqa::QdSmem) + 2048) <= 233472, "two CTAs per SM");
+    const size_t smem = sizeof(sgqa::QdSmem) + 1024;
+    auto kern = acc != nullptr ? sgqa::attn_q8_decode_kernel<true> : sgqa::attn_q8_decode_kernel<false>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * nsplit));
+    cfg.blockDim = dim3(sgqa::kQdThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(nsplit);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m, static_cast<const __nv_bfloat16*>(q), c.scale, sel, sel_count,
+                                       static_cast<const __nv_bfloat16*>(gate), static_cast<__nv_bfloat16*>(out), wt, nq,
+                                       p->num_kv_groups, p->topk, q0, c.blocks, nsplit, scale_log2);
+    if (e != cudaSuccess) return cuda_fail(e, "attn_q8_decode_kernel launch");
+    SGQA_LAUNCH_CHECK("attn_q8_decode_kernel");
+    return SGQA_OK;
+  }
   const size_t smem = sizeof(sgqa::Q8SimpleSmem);
   cudaFuncSetAttribute(sgqa::attn_q8_simple_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   sgqa::attn_q8_simple_kernel<<<static_cast<unsigned>(rows), sgqa::kQ8SimpleThreads, smem, st>>>(
       static_cast<const __nv_bfloat16*>(q), c.kv8, c.scale, sel, sel_count, static_cast<const __nv_bfloat16*>(gate),
-      static_cast<__nv_bfloat16*>(out), acc, nq, p->num_kv_groups, p->topk, q0, c.blocks,
-      softmax_scale(p) * 1.4426950408889634f);
+      static_cast<__nv_bfloat16*>(out), acc, nq, p->num_kv_groups, p->topk, q0, c.blocks, scale_log2);
   SGQA_LAUNCH_CHECK("attn_q8_simple_kernel");
   return SGQA_OK;
 }

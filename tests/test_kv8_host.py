@@ -171,3 +171,70 @@ def test_reference_eviction_by_hand():
     # kept: 0 (protected, slot 2), 12 (protected, slot 5), weight 9 (slot 4), weight 5 with the smaller number 9 (slot 0)
     assert src == [0, 4, 2, 5, 6] and num == [9, 11, 0, 12]
     assert list(acc) == [5, 9, 0, 2, 77, 0, 0]
+
+
+class _Tensor:
+    """Looks like a CUDA tensor to the binding's checks."""
+    def __init__(self, shape, dtype, device="cuda:1", contiguous=True, cuda=True):
+        self.shape, self.dtype, self.device = shape, dtype, torch.device(device)
+        self.is_cuda, self._c = cuda, contiguous
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return self._c
+
+    def data_ptr(self):
+        return PTR
+
+
+def _append_tensors(**kw):
+    t = dict(k=_Tensor((2, 3, 4, 192), torch.bfloat16), v=_Tensor((2, 3, 4, 192), torch.bfloat16),
+             tail=_Tensor((2, 2, 8, 4, 192), torch.bfloat16), kv8=_Tensor((2, 8, 4, 2, 8, 192), torch.uint8),
+             kv_scale=_Tensor((2, 8, 4, 2), torch.float32))
+    t.update(kw)
+    return t
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=_Tensor((2, 2, 4, 192), torch.bfloat16)), dict(v=_Tensor((2, 3, 4, 192), torch.float32)),
+    dict(tail=_Tensor((2, 2, 8, 4, 192), torch.bfloat16, contiguous=False)),
+    dict(kv8=_Tensor((2, 8, 4, 2, 8, 192), torch.uint8, cuda=False)), dict(kv_scale=_Tensor((2, 8, 4), torch.float32))])
+def test_tensors_that_do_not_fit_are_refused(kw):
+    with pytest.raises(ValueError):
+        Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **_append_tensors(**kw))
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    class Guard:
+        def __init__(self, dev):
+            log.append(("enter", str(dev)))
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *a):
+            log.append("exit")
+
+    class Stream:
+        cuda_stream, device = 77, torch.device("cuda:1")
+
+    log = []
+    monkeypatch.setattr(Bd.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(Bd.torch.cuda, "device", Guard)
+    monkeypatch.setattr(Bd.torch.cuda, "current_stream", lambda dev: Stream())
+    monkeypatch.setattr(Bd._lib, "sgqa_kv_append_q8", lambda *a: log.append(("call", a[-1])) or 0)
+    Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **_append_tensors())
+    assert log == [("enter", "cuda:1"), ("call", 77), "exit"]
+    monkeypatch.setattr(Bd.torch.cuda, "current_device", lambda: 1)
+    log.clear()
+    Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **_append_tensors())
+    assert log == [("call", 77)]
+    other = Stream()
+    other.device = torch.device("cuda:0")
+    with pytest.raises(ValueError):
+        Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, stream=other, **_append_tensors())

@@ -55,44 +55,50 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
 // computes transposed, so that the 16 heads are the narrow MMA side:
 //   S^T [128 tokens x 32] = K [128 x 192] Q^T     6 MMAs (M128 N32 K32): columns
 //                           16 heads' hi | 16 heads' lo; K as gathered (K-major)
-//   softmax               one thread per token, 16 heads in registers
+//   softmax               one thread per token and half of the heads
 //   O^T [192 dims x 32] += V^T [192 x 128] P^T    2 x 4 MMAs (M128 N32 K32): V as
 //                           gathered (MN-major), dims 0-127 and 64-191 (the rows
 //                           computed twice are not read); P through shared memory
-// A token's max over heads never crosses threads: the reference moves only when
-// some weight exceeds 2^8 (one barrier-or per tile tells), and only then are
-// the 16 maxima reduced over the tile and O rescaled in TMEM.
-// One box (3 KB: a block's K and V) per block, issued by 16 lanes side by
-// side; K and V share a stage.  The splits of a row form one cluster and
+// A token's scores never cross threads for a maximum: the reference moves only
+// when some weight exceeds 2^8 (one barrier-or per tile tells), and only then
+// are a head's maxima reduced over the tile and O rescaled in TMEM.
+// K and V are gathered by a warp each (16 lanes, one 1.5 KB box per block) into
+// rings of their own: a K stage is free again after its MMA, a V stage only
+// after the softmax of its tile.  The splits of a row form one cluster and
 // combine through distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int kQdTile = 16;       // blocks per tile
-constexpr int kQdStages = 2;
-constexpr int kQdThreads = 224;   // producer, QK issuer, 4 softmax warps, PV issuer
+constexpr int kQdStages = 2;      // of K and of V
+constexpr int kQdMeta = 4;        // tiles whose scales and masks are held
+constexpr int kQdThreads = 384;   // K and V producers, QK and PV issuers, 8 softmax warps
 constexpr int kQdCols = 128;      // TMEM: S 2 x 32, O 2 x 32
 constexpr int kQdMaxSplit = 8;    // splits of a row = one (portable) cluster
+constexpr int kQdStage = kQdTile * kQ8Half;  // bytes of a stage
 
 struct __align__(1024) QdSmem {
-  uint8_t kv[kQdStages][kQdTile][3][16][64];  // [block][chunk of 64 dims][8 K rows, 8 V rows][64 B], 64-byte swizzle
+  uint8_t k[kQdStages][kQdTile][3][8][64];    // [block][chunk of 64 dims][8 rows][64 B], 64-byte swizzle
+  uint8_t v[kQdStages][kQdTile][3][8][64];
   uint8_t q[3][32][64];                       // [chunk][16 hi, 16 lo][64 B], 64-byte swizzle
   uint8_t p[2][kQdTile * kQ8Tok][32];         // [token][16 hi, 16 lo], 32-byte swizzle
-  float2 scale[kQdStages][kQdTile];           // K and V scale of a stage's blocks
-  uint32_t mask[kQdStages][kQdTile];          // their attended tokens
-  float wmax[4][kHg];                         // a reference change: maxima of the four warps
+  float4 meta[kQdMeta][kQdTile];              // a tile's blocks: K scale, V scale, its log2, attended tokens (bits)
+  float wmax[4][kHg];                         // a reference change: maxima of the four lane quadrants
   float qscale[kHg];
-  uint64_t full[kQdStages], empty[kQdStages], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, o_final, drain[2];
+  uint64_t k_full[kQdStages], k_empty[kQdStages], v_full[kQdStages], v_empty[kQdStages], meta_full[kQdMeta];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, o_final, drain[2];
   uint32_t tmem;
   int abort;
 };
 
-// The combine's view of the ring, once the last MMA is done.
+// The combine's view of the K ring, once the last MMA is done.
 struct QdOut {
   float m[kHg], l[kHg];            // this split's reference and sum
   float f[kQdMaxSplit][kHg];       // factor of every split
   float fin[kHg], wfac[kHg];       // normalisation (and gate); weight normalisation
+  float mu[kHg];                   // the splits' common reference
   float wl[4][kHg];
   float o[kHg][kD + 1];
 };
+static_assert(sizeof(QdOut) <= kQdStages * kQdStage, "the combine fits the K ring");
 
 // Workspace of the weights: per (row, block of the row) 16 heads' sums, then per
 // (row, tile) the references they refer to.
@@ -119,85 +125,99 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
   const int64_t i = (row / G) % nq;
   const int64_t seq = row / (G * nq);
   const int64_t t = q_pos0 + i, hist = t / kQ8Tok;
-  const int cnt = min(max(sel_count[row], 0), k);
   const int32_t* ids = sel + row * k;
-  const int nblk = cnt + 1;  // selected blocks, then the current block
-  const int per = (nblk + nsplit - 1) / nsplit;
-  const int b0 = min(nblk, split * per), b1 = min(nblk, b0 + per);
+  // Positions [0, kh) are the list's (kh: the longest it can be; positions from
+  // the count on are empty), position kh is the current block.  The split does
+  // not wait for the count.
+  const int kh = static_cast<int>(min(static_cast<int64_t>(k), hist));
+  const int per = (kh + nsplit) / nsplit;
+  const int b0 = min(kh + 1, split * per), b1 = min(kh + 1, b0 + per);
   const int n_tiles = (b1 - b0 + kQdTile - 1) / kQdTile;
   volatile int* abort = &sm.abort;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  // block at position b: -1 none, -2 an id that breaks the contract
+  auto block_at = [&](int b, int cnt, int id, int prev) -> int32_t {
+    if (b >= b1) return -1;
+    if (b == kh) return static_cast<int32_t>(hist);
+    if (b >= cnt) return -1;
+    return id < 0 || id >= hist || id <= prev ? -2 : id;
+  };
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int s = 0; s < kQdStages; ++s) {
-      tc::mbar_init(bar(sm.full[s]), kQdTile);
-      tc::mbar_init(bar(sm.empty[s]), 1);
+      tc::mbar_init(bar(sm.k_full[s]), kQdTile);
+      tc::mbar_init(bar(sm.v_full[s]), kQdTile);
+      tc::mbar_init(bar(sm.k_empty[s]), 1);
+      tc::mbar_init(bar(sm.v_empty[s]), 1);
     }
+    for (int s = 0; s < kQdMeta; ++s) tc::mbar_init(bar(sm.meta_full[s]), kQdTile);
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(sm.s_full[b]), 1);
-      tc::mbar_init(bar(sm.s_free[b]), 128);
-      tc::mbar_init(bar(sm.p_full[b]), 128);
+      tc::mbar_init(bar(sm.s_free[b]), 256);
+      tc::mbar_init(bar(sm.p_full[b]), 256);
       tc::mbar_init(bar(sm.pv_done[b]), 1);
       tc::mbar_init(bar(sm.drain[b]), 1);
     }
-    tc::mbar_init(bar(sm.q_full), 128);
+    tc::mbar_init(bar(sm.q_full), 256);
     tc::mbar_init(bar(sm.o_final), 1);
     tc::mbar_fence_init();
+  }
+  // the producers' first ids, before the barrier
+  int id1 = -1, prev1 = -1, id2 = -1, prev2 = -1, cnt = 0;
+  auto fetch = [&](int j, int& id, int& prev) {
+    const int b = b0 + j * kQdTile + lane;
+    id = prev = -1;
+    if (lane < kQdTile && b < min(b1, kh)) {
+      id = __ldg(ids + b);
+      if (b > 0) prev = __ldg(ids + b - 1);
+    }
+  };
+  if (warp == 0 || warp == 11) {
+    fetch(0, id1, prev1);
+    fetch(1, id2, prev2);
+    cnt = min(max(__ldg(sel_count + row), 0), k);
   }
   if (warp == 1) tc::tmem_alloc(smem_u32(&sm.tmem), kQdCols);
   __syncthreads();
   tc::fence_after();
   const uint32_t tS = sm.tmem, tO = sm.tmem + 64;
-  int issued = 0;  // producer: tiles whose copies this warp issued
+  int issued = 0;  // producers: tiles whose copies this warp issued
 
   // per-head state of the softmax threads
-  float ref[kHg], l[kHg];
+  float ref[8], l[8];
 #pragma unroll
-  for (int h = 0; h < kHg; ++h) { ref[h] = -INFINITY; l[h] = 0.f; }
+  for (int h = 0; h < 8; ++h) { ref[h] = -INFINITY; l[h] = 0.f; }
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer
+  if (warp == 0 || warp == 11) {
+    // ---------------------------------------------------------------- producers
+    const bool is_k = warp == 0;
     if (lane == 0) tc::prefetch_tmap(&kvmap);
-    // block of position b (-1: none): ids and their predecessors are fetched
-    // two tiles ahead, the scales one
-    auto fetch = [&](int j, int& id, int& prev) {
-      const int b = b0 + j * kQdTile + lane;
-      id = prev = -1;
-      if (lane < kQdTile && b < b1 && b < cnt) {
-        id = __ldg(ids + b);
-        if (b > 0) prev = __ldg(ids + b - 1);
-      }
-    };
+    // ids are fetched two tiles ahead, scales one
     auto resolve = [&](int j, int id, int prev) -> int32_t {
-      const int b = b0 + j * kQdTile + lane;
-      if (lane >= kQdTile || b >= b1) return -1;
-      if (b == cnt) return static_cast<int32_t>(hist);
-      if (id < 0 || id >= hist || id <= prev) {
-        report(kDevBounds);
-        return -1;
-      }
-      return id;
+      int32_t blk = block_at(lane < kQdTile ? b0 + j * kQdTile + lane : b1, cnt, id, prev);
+      if (blk == -2 && is_k) report(kDevBounds);
+      return blk;
     };
     auto scales = [&](int32_t blk) -> float2 {
-      return blk >= 0 ? __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g) : make_float2(0.f, 1.f);
+      return is_k && blk >= 0 ? __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g)
+                              : make_float2(0.f, 1.f);
     };
-    int id1, prev1, id2, prev2;
-    fetch(0, id1, prev1);
-    fetch(1, id2, prev2);
     int32_t blk = resolve(0, id1, prev1);
     float2 sc = scales(blk);
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % kQdStages;
-      if (j >= kQdStages && !tc::warp_wait(bar(sm.empty[s]), ((j / kQdStages) - 1) & 1, abort)) break;
+      if (j >= kQdStages && !tc::warp_wait(bar(is_k ? sm.k_empty[s] : sm.v_empty[s]), ((j / kQdStages) - 1) & 1, abort)) break;
       if (lane < kQdTile) {
-        const uint32_t full = bar(sm.full[s]);
-        tc::mbar_expect_only(full, kQ8Blk);
+        const uint32_t full = bar(is_k ? sm.k_full[s] : sm.v_full[s]);
+        tc::mbar_expect_tx(full, kQ8Half);
         // no block: a box outside the cache, filled with zeros
-        tc::tma_load_5d(smem_u32(&sm.kv[s][lane][0][0][0]), &kvmap, 0, 0, 0, blk >= 0 ? g : 0,
-                        blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
-        sm.scale[s][lane] = sc;
-        sm.mask[s][lane] = blk < 0 ? 0u : blk == hist ? (2u << (t % kQ8Tok)) - 1u : 0xFFu;
-        tc::mbar_arrive(full);
+        tc::tma_load_5d(smem_u32(is_k ? &sm.k[s][lane][0][0][0] : &sm.v[s][lane][0][0][0]), &kvmap, 0, is_k ? 0 : kQ8Tok, 0,
+                        blk >= 0 ? g : 0, blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
+        if (is_k) {
+          const uint32_t m = blk < 0 ? 0u : blk == hist ? (2u << (t % kQ8Tok)) - 1u : 0xFFu;
+          sm.meta[j % kQdMeta][lane] = make_float4(sc.x, m != 0 ? sc.y : 0.f, m != 0 ? log2f(sc.y) : 0.f, __uint_as_float(m));
+          tc::mbar_arrive(bar(sm.meta_full[j % kQdMeta]));
+        }
       }
       __syncwarp();
       issued = j + 1;
@@ -208,47 +228,49 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S^T = K Q^T
     const uint32_t id_qk = tc::idesc_e4m3(128, 32, false, false);
-    const uint64_t dk0 = tc::sdesc(smem_u32(&sm.kv[0][0][0][0][0]), 16, kQ8Blk, tc::kSw64);
+    const uint64_t dk0 = tc::sdesc(smem_u32(&sm.k[0][0][0][0][0]), 16, kQ8Half, tc::kSw64);
     const uint64_t dq0 = tc::sdesc(smem_u32(&sm.q[0][0][0]), 16, 512, tc::kSw64);
     bool ok = tc::warp_wait(bar(sm.q_full), 0, abort);
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kQdStages, b = j & 1;
-      ok = tc::warp_wait(bar(sm.full[s]), (j / kQdStages) & 1, abort);
+      ok = tc::warp_wait(bar(sm.k_full[s]), (j / kQdStages) & 1, abort);
       if (ok && j >= 2) ok = tc::warp_wait(bar(sm.s_free[b]), ((j >> 1) - 1) & 1, abort);
       if (!ok) break;
       tc::fence_after();
       if (tc::elect_one()) {
-        const uint64_t dk = dk0 + (kQdTile * kQ8Blk / 16) * s;
+        const uint64_t dk = dk0 + (kQdStage / 16) * s;
 #pragma unroll
-        for (int kk = 0; kk < 6; ++kk)  // K: +1 KB per 64 dims; Q: +2 KB; both +32 B per 32 dims
-          tc::mma_f8(tS + 32 * b, dk + (kk >> 1) * 64 + (kk & 1) * 2, dq0 + (kk >> 1) * 128 + (kk & 1) * 2, id_qk,
+        for (int kk = 0; kk < 6; ++kk)  // K: +512 B per 64 dims; Q: +2 KB; both +32 B per 32 dims
+          tc::mma_f8(tS + 32 * b, dk + (kk >> 1) * 32 + (kk & 1) * 2, dq0 + (kk >> 1) * 128 + (kk & 1) * 2, id_qk,
                      kk > 0 ? 1u : 0u);
         tc::mma_commit(bar(sm.s_full[b]));
+        tc::mma_commit(bar(sm.k_empty[s]));
       }
       __syncwarp();
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ---------------------------------------------------------------- O^T += V^T P^T
     const uint32_t id_pv = tc::idesc_e4m3(128, 32, true, true);
-    // V: 64-dim chunks 1 KB apart, 8-token groups one block apart; P: 8-token groups 256 B apart
-    const uint64_t dv0 = tc::sdesc(smem_u32(&sm.kv[0][0][0][8][0]), 1024, kQ8Blk, tc::kSw64);
+    // V: 64-dim chunks 512 B apart, 8-token groups one block apart; P: 8-token groups 256 B apart
+    const uint64_t dv0 = tc::sdesc(smem_u32(&sm.v[0][0][0][0][0]), 512, kQ8Half, tc::kSw64);
     const uint64_t dp0 = tc::sdesc(smem_u32(&sm.p[0][0][0]), 256, 256, tc::kSw32);
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kQdStages, b = j & 1;
-      ok = tc::warp_wait(bar(sm.p_full[b]), (j >> 1) & 1, abort);
+      ok = tc::warp_wait(bar(sm.v_full[s]), (j / kQdStages) & 1, abort) &&
+           tc::warp_wait(bar(sm.p_full[b]), (j >> 1) & 1, abort);
       if (!ok) break;
       tc::fence_after();
       if (tc::elect_one()) {
-        const uint64_t dv = dv0 + (kQdTile * kQ8Blk / 16) * s;
+        const uint64_t dv = dv0 + (kQdStage / 16) * s;
         const uint64_t dp = dp0 + (kQdTile * kQ8Tok * 32 / 16) * b;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // 32 tokens: V +4 blocks, P +1 KB
           const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
-          tc::mma_f8(tO, dv + kk * (4 * kQ8Blk / 16), dp + kk * 64, id_pv, acc);
-          tc::mma_f8(tO + 32, dv + 64 + kk * (4 * kQ8Blk / 16), dp + kk * 64, id_pv, acc);
+          tc::mma_f8(tO, dv + kk * (4 * kQ8Half / 16), dp + kk * 64, id_pv, acc);
+          tc::mma_f8(tO + 32, dv + 32 + kk * (4 * kQ8Half / 16), dp + kk * 64, id_pv, acc);
         }
-        tc::mma_commit(bar(sm.empty[s]));
+        tc::mma_commit(bar(sm.v_empty[s]));
         tc::mma_commit(bar(sm.pv_done[b]));
         if (j + 1 == n_tiles) tc::mma_commit(bar(sm.o_final));
       }
@@ -256,13 +278,15 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const int sw = warp - 2, quad = warp & 3;
+    // Warps 2-5 take heads 0-7, warps 6-9 heads 8-15; the four warps of a half
+    // (one per TMEM lane quadrant) agree on its references by a barrier of their own.
+    const int sw = warp - 2, quad = warp & 3, half = sw >> 2, h0 = 8 * half, hbar = 1 + half;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int tok = quad * 32 + lane;  // token of the tile = TMEM lane
-    // queries: a warp packs four heads, a lane dims 2 lane, 2 lane + 1 of every chunk
+    // queries: a warp packs two heads, a lane dims 2 lane, 2 lane + 1 of every chunk
 #pragma unroll
-    for (int hh = 0; hh < 4; ++hh) {
-      const int h = 4 * sw + hh;
+    for (int hh = 0; hh < 2; ++hh) {
+      const int h = h0 + 2 * (sw & 3) + hh;
       const uint32_t* src = reinterpret_cast<const uint32_t*>(q + (row * kHg + h) * kD);
       float x[3][2], mx = 0.f;
       bool fin = true;
@@ -290,53 +314,53 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     }
     tc::fence_proxy_async_smem();
     tc::mbar_arrive(bar(sm.q_full));
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    float rc[kHg];
+    asm volatile("bar.sync %0, 128;" ::"r"(hbar) : "memory");
+    float rc[8];
 #pragma unroll
-    for (int h = 0; h < kHg; ++h) rc[h] = sm.qscale[h];
+    for (int h = 0; h < 8; ++h) rc[h] = sm.qscale[h0 + h];
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      const int s = j % kQdStages, b = j & 1;
-      ok = ok && tc::mbar_wait(bar(sm.full[s]), (j / kQdStages) & 1, abort);
-      const float2 sc = sm.scale[s][tok >> 3];
-      const bool use = (sm.mask[s][tok >> 3] >> (tok & 7)) & 1u;
-      const float lvs = use ? log2f(sc.y) : 0.f;
+      const int b = j & 1;
+      ok = ok && tc::mbar_wait(bar(sm.meta_full[j % kQdMeta]), (j / kQdMeta) & 1, abort);
+      const float4 meta = sm.meta[j % kQdMeta][tok >> 3];
+      const bool use = (__float_as_uint(meta.w) >> (tok & 7)) & 1u;
       ok = ok && tc::mbar_wait(bar(sm.s_full[b]), (j >> 1) & 1, abort);
       tc::fence_after();
-      uint32_t sr[32];
-      tc::tmem_ld32(tS + 32 * b + lane_off, sr);
+      uint32_t sh[8], sl[8];
+      tc::tmem_ld8(tS + 32 * b + lane_off + h0, sh);
+      tc::tmem_ld8(tS + 32 * b + lane_off + 16 + h0, sl);
       tc::tmem_ld_wait();
       tc::fence_before();
       tc::mbar_arrive(bar(sm.s_free[b]));
-      float x[kHg];
+      float x[8];
       bool grow = false;
 #pragma unroll
-      for (int h = 0; h < kHg; ++h) {
-        const float v = fmaf(__uint_as_float(sr[16 + h]), 0.0625f, __uint_as_float(sr[h])) * (sc.x * rc[h]);
+      for (int h = 0; h < 8; ++h) {
+        const float v = fmaf(__uint_as_float(sl[h]), 0.0625f, __uint_as_float(sh[h])) * (meta.x * rc[h]);
         x[h] = use ? v : -INFINITY;
-        grow = grow || x[h] + lvs > ref[h] + 8.f;
+        grow = grow || x[h] + meta.z > ref[h] + 8.f;
       }
       // does any weight of the tile exceed 2^8?
       int any;
       asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
+          "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
           : "=r"(any)
-          : "r"(static_cast<int>(grow))
+          : "r"(static_cast<int>(grow)), "r"(hbar)
           : "memory");
       if (any) {
         // new references: the largest score (plus log2 of its V scale) - 4, so that
-        // weights stay between 2^4 and 2^8 at most
+        // the largest weights stay between 2^4 and 2^8
 #pragma unroll
-        for (int h = 0; h < kHg; ++h) {
-          const int v = __float_as_int(fmaxf(x[h] + lvs, -INFINITY));
+        for (int h = 0; h < 8; ++h) {
+          const int v = __float_as_int(fmaxf(x[h] + meta.z, -INFINITY));
           const int mx = __reduce_max_sync(0xffffffffu, v ^ ((v >> 31) & 0x7FFFFFFF));
-          if (lane == 0) sm.wmax[sw][h] = __int_as_float(mx ^ ((mx >> 31) & 0x7FFFFFFF));
+          if (lane == 0) sm.wmax[quad][h0 + h] = __int_as_float(mx ^ ((mx >> 31) & 0x7FFFFFFF));
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        float al[kHg];
+        asm volatile("bar.sync %0, 128;" ::"r"(hbar) : "memory");
+        float al[8];
 #pragma unroll
-        for (int h = 0; h < kHg; ++h) {
-          const float mx = fmaxf(fmaxf(sm.wmax[0][h], sm.wmax[1][h]), fmaxf(sm.wmax[2][h], sm.wmax[3][h]));
+        for (int h = 0; h < 8; ++h) {
+          const float mx = fmaxf(fmaxf(sm.wmax[0][h0 + h], sm.wmax[1][h0 + h]), fmaxf(sm.wmax[2][h0 + h], sm.wmax[3][h0 + h]));
           const float nr = mx > ref[h] + 8.f ? mx - 4.f : ref[h];
           al[h] = nr == ref[h] ? 1.f : exp2f(ref[h] - nr);
           ref[h] = nr;
@@ -346,31 +370,28 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, abort);
           tc::fence_after();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + 32 * half + lane_off, o);
+          for (int part = 0; part < 4; ++part) {  // dims 0-127, 64-191; hi, lo columns
+            uint32_t o[8];
+            const uint32_t at = tO + 16 * part + h0 + lane_off;
+            tc::tmem_ld8(at, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * al[h & 15]);
-            tc::tmem_st32(tO + 32 * half + lane_off, o);
+            for (int h = 0; h < 8; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * al[h]);
+            tc::tmem_st8(at, o);
           }
           tc::tmem_st_wait();
         }
       }
-      uint32_t hi[4], lo[4];
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int h = 0; h < kHg; h += 2) {
-        float pl[2];
+      for (int h = 0; h < 8; h += 2) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float r = ref[h + e] == -INFINITY ? 0.f : ref[h + e];
-          pl[e] = fast_exp2(x[h + e] - r);
-          l[h + e] += pl[e];
-          x[h + e] = pl[e];
+          x[h + e] = fast_exp2(x[h + e] - (ref[h + e] == -INFINITY ? 0.f : ref[h + e]));
+          l[h + e] += x[h + e];
         }
         uint32_t a, c;
-        const float vs = use ? sc.y : 0.f;
-        split_e4m3(pl[0] * vs, pl[1] * vs, a, c, 16.f);
+        split_e4m3(x[h] * meta.y, x[h + 1] * meta.y, a, c, 16.f);
         if (h & 2) {
           hi[h >> 2] |= a << 16;
           lo[h >> 2] |= c << 16;
@@ -382,32 +403,30 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       // P buffer b is free once O += P(j-2) V(j-2) has read it
       if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j >> 1) - 1) & 1, abort);
       {
-        uint8_t* pr = &sm.p[b][tok][0];
-        const uint32_t sw = ((tok >> 2) & 1) << 4;
-        *reinterpret_cast<uint4*>(pr + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(pr + (16 ^ sw)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        uint8_t* pr = &sm.p[b][tok][0] + h0;
+        const uint32_t swz = ((tok >> 2) & 1) << 4;
+        *reinterpret_cast<uint2*>(pr + swz) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(pr + (16 ^ swz)) = make_uint2(lo[0], lo[1]);
       }
       tc::fence_proxy_async_smem();
       tc::fence_before();
       tc::mbar_arrive(bar(sm.p_full[b]));
       if (WEIGHTS) {
         // sums over the block's eight tokens (lanes): every exchange halves the
-        // heads a lane holds; lane r of a block ends with heads 2 r, 2 r + 1
-        float y[8], z[4], w2[2];
+        // heads a lane holds; lane r of a block ends with head r
+        float y[4], z[2];
         const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) y[c] = (h4 ? x[8 + c] : x[c]) + __shfl_xor_sync(0xffffffffu, h4 ? x[c] : x[8 + c], 4);
+        for (int c = 0; c < 4; ++c) y[c] = (h4 ? x[4 + c] : x[c]) + __shfl_xor_sync(0xffffffffu, h4 ? x[c] : x[4 + c], 4);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) z[c] = (h2 ? y[4 + c] : y[c]) + __shfl_xor_sync(0xffffffffu, h2 ? y[c] : y[4 + c], 2);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) w2[c] = (h1 ? z[2 + c] : z[c]) + __shfl_xor_sync(0xffffffffu, h1 ? z[c] : z[2 + c], 1);
+        for (int c = 0; c < 2; ++c) z[c] = (h2 ? y[2 + c] : y[c]) + __shfl_xor_sync(0xffffffffu, h2 ? y[c] : y[2 + c], 2);
+        const float w = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
         const int blk = b0 + j * kQdTile + (tok >> 3);
-        if (blk < b1)
-          *reinterpret_cast<float2*>(wts.sums + (row * (k + 1) + blk) * kHg + 2 * (lane & 7)) = make_float2(w2[0], w2[1]);
+        if (blk < b1) wts.sums[(row * (k + 1) + blk) * kHg + h0 + (lane & 7)] = w;
         if (tok == 0) {
-          float* r = wts.refs + (row * wts.tiles + split * (wts.tiles / nsplit) + j) * kHg;
+          float* r = wts.refs + (row * wts.tiles + split * (wts.tiles / nsplit) + j) * kHg + h0;
 #pragma unroll
-          for (int h = 0; h < kHg; ++h) r[h] = ref[h];
+          for (int h = 0; h < 8; ++h) r[h] = ref[h];
         }
       }
     }
@@ -417,44 +436,47 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
   // path the copies and MMAs in flight land before their memory is reused.
   __syncthreads();
   if (sm.abort) {
-    if (warp == 0) {
-      for (int j = max(issued - kQdStages, 0); j < issued; ++j) tc::mbar_drain(bar(sm.full[j % kQdStages]), (j / kQdStages) & 1);
-    } else if (warp == 1 || warp == 6) {
+    if (warp == 0 || warp == 11) {
+      for (int j = max(issued - kQdStages, 0); j < issued; ++j)
+        tc::mbar_drain(bar(warp == 0 ? sm.k_full[j % kQdStages] : sm.v_full[j % kQdStages]), (j / kQdStages) & 1);
+    } else if (warp == 1 || warp == 10) {
       uint64_t& d = sm.drain[warp == 1 ? 0 : 1];
       if (tc::elect_one()) tc::mma_commit(bar(d));
       __syncwarp();
       tc::mbar_drain(bar(d), 0);
     }
+    __syncthreads();
   }
-  __syncthreads();
-  QdOut& po = *reinterpret_cast<QdOut*>(&sm.kv[0][0][0][0][0]);
-  if (warp >= 2 && warp <= 5) {
-    const int quad = warp & 3;
+  QdOut& po = *reinterpret_cast<QdOut*>(&sm.k[0][0][0][0][0]);
+  if (warp >= 2 && warp <= 9) {
+    const int quad = warp & 3, h0 = 8 * ((warp - 2) >> 2);
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     if (n_tiles > 0) {
       tc::fence_after();
       const int d = quad * 32 + lane;
-      uint32_t o[32];
-      tc::tmem_ld32(tO + lane_off, o);
+      uint32_t hi[8], lo[8];
+      tc::tmem_ld8(tO + h0 + lane_off, hi);
+      tc::tmem_ld8(tO + 16 + h0 + lane_off, lo);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int h = 0; h < kHg; ++h) po.o[h][d] = fmaf(__uint_as_float(o[16 + h]), 0.0625f, __uint_as_float(o[h]));
+      for (int h = 0; h < 8; ++h) po.o[h0 + h][d] = fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h]));
       if (quad >= 2) {
-        tc::tmem_ld32(tO + 32 + lane_off, o);
+        tc::tmem_ld8(tO + 32 + h0 + lane_off, hi);
+        tc::tmem_ld8(tO + 48 + h0 + lane_off, lo);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < kHg; ++h) po.o[h][64 + d] = fmaf(__uint_as_float(o[16 + h]), 0.0625f, __uint_as_float(o[h]));
+        for (int h = 0; h < 8; ++h) po.o[h0 + h][64 + d] = fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h]));
       }
     } else {
-      for (int x = threadIdx.x - 64; x < kHg * (kD + 1); x += 128) (&po.o[0][0])[x] = 0.f;
+      for (int x = threadIdx.x - 64; x < kHg * (kD + 1); x += 256) (&po.o[0][0])[x] = 0.f;
     }
 #pragma unroll
-    for (int h = 0; h < kHg; ++h) {
+    for (int h = 0; h < 8; ++h) {
       float v = l[h];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) po.wl[warp - 2][h] = v;
-      if (warp == 2 && lane == 0) po.m[h] = ref[h];
+      if (lane == 0) po.wl[quad][h0 + h] = v;
+      if (quad == 0 && lane == 0) po.m[h0 + h] = ref[h];
     }
     tc::fence_before();
   }
@@ -463,7 +485,8 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     tc::fence_after();
     tc::tmem_dealloc(sm.tmem, kQdCols);
   }
-  if (threadIdx.x < kHg) po.l[threadIdx.x] = (po.wl[0][threadIdx.x] + po.wl[1][threadIdx.x]) + (po.wl[2][threadIdx.x] + po.wl[3][threadIdx.x]);
+  if (threadIdx.x < kHg)
+    po.l[threadIdx.x] = (po.wl[0][threadIdx.x] + po.wl[1][threadIdx.x]) + (po.wl[2][threadIdx.x] + po.wl[3][threadIdx.x]);
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
@@ -480,8 +503,8 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       ls += lr == 0.f ? 0.f : a * lr;
     }
     po.fin[h] = gate_factor(gate, row * kHg + h) / ls;
-    // a weight sum with reference r counts 2^(r - mu) / ls
-    if (WEIGHTS) po.wfac[h] = 1.f / ls;
+    po.wfac[h] = 1.f / ls;  // a weight sum with reference r counts 2^(r - mu) / ls
+    po.mu[h] = mu;
   }
   __syncthreads();
   {
@@ -496,27 +519,18 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     }
   }
   if (WEIGHTS) {
-    // the common reference (largest of the splits')
-    float mu[kHg];
-    if (static_cast<int>(threadIdx.x) < b1 - b0) {
-#pragma unroll
-      for (int h = 0; h < kHg; ++h) {
-        float mm = -INFINITY;
-        for (int r = 0; r < nsplit; ++r) mm = fmaxf(mm, cluster.map_shared_rank(po.m, r)[h]);
-        mu[h] = mm == -INFINITY ? 0.f : mm;
-      }
-    }
+    const int n_cnt = min(max(sel_count[row], 0), k);
     for (int x = threadIdx.x; x < b1 - b0; x += kQdThreads) {
       const int b = b0 + x;
-      const int64_t blk = b == cnt ? hist : ids[b];
-      if (blk < 0 || blk > hist || (b < cnt && (blk == hist || (b > 0 && blk <= ids[b - 1])))) continue;  // reported
+      const int32_t blk = block_at(b, n_cnt, b < kh ? ids[b] : 0, b > 0 && b < kh ? ids[b - 1] : -1);
+      if (blk < 0) continue;
       const float* ws = wts.sums + (row * (k + 1) + b) * kHg;
       const float* rs = wts.refs + (row * wts.tiles + split * (wts.tiles / nsplit) + x / kQdTile) * kHg;
       float w = 0.f;
 #pragma unroll
       for (int h = 0; h < kHg; ++h) {
         const float v = ws[h];
-        w += v == 0.f ? 0.f : v * exp2f((rs[h] == -INFINITY ? 0.f : rs[h]) - mu[h]) * po.wfac[h];
+        w += v == 0.f ? 0.f : v * exp2f((rs[h] == -INFINITY ? 0.f : rs[h]) - po.mu[h]) * po.wfac[h];
       }
       acc_add(wts.acc + seq * blocks + blk, w);
     }

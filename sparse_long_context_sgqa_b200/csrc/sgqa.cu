@@ -686,12 +686,12 @@ size_t attn_q8_ws_bytes(const sgqa_params* p, int64_t S, int64_t nq, bool weight
 }
 
 // Tensor map of the cache as (64 codes, rows of K then V, chunk of 64 dims, group, block).
-sgqa_status q8_map(const Q8Cache& c, int G, int64_t S, int rows, CUtensorMap* m) {
+sgqa_status q8_map(const Q8Cache& c, int G, int64_t S, CUtensorMap* m) {
   auto enc = tmap_encoder();
   if (enc == nullptr) return fail(SGQA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   cuuint64_t dims[5] = {64, 2 * sgqa::kQ8Tok, 3, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(S * c.blocks)};
   cuuint64_t strides[4] = {sgqa::kD, 64, sgqa::kQ8Blk, static_cast<cuuint64_t>(G) * sgqa::kQ8Blk};
-  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(rows), 3, 1, 1};
+  cuuint32_t box[5] = {64, sgqa::kQ8Tok, 3, 1, 1};  // a block's K or V
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(c.kv8), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -715,10 +715,10 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
   const Q8Ws w = attn_q8_ws(p, S, nq, acc != nullptr);
   if (nq <= kDecodeMaxNq) {
     CUtensorMap m;
-    sgqa_status s = q8_map(c, p->num_kv_groups, S, 2 * sgqa::kQ8Tok, &m);
+    sgqa_status s = q8_map(c, p->num_kv_groups, S, &m);
     if (s != SGQA_OK) return s;
     const int nsplit = q8_splits(p, rows, q0 + nq);
-    const int per = (std::min<int>(p->topk, static_cast<int>(std::min<int64_t>((q0 + nq - 1) / sgqa::kQ8Tok, p->topk))) + nsplit) / nsplit;
+    const int per = (static_cast<int>(std::min<int64_t>((q0 + nq - 1) / sgqa::kQ8Tok, p->topk)) + nsplit) / nsplit;
     sgqa::QdWeights wt{};
     if (acc != nullptr) {
       wt.acc = acc;

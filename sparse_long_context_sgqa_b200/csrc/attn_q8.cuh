@@ -9,10 +9,10 @@
 // both.  With one scale per (block, group), a block's K scale multiplies its
 // scores and its V scale its weights.
 //
-// Softmax reference.  The weights that enter the MMA are 2^(s + log2 vs - ref):
-// the reference follows the scores plus the logarithm of the V scale, so that
-// blocks of small values keep their bits where they carry the result.  The sum
-// of the weights, FP32, uses the same reference without the V scale.
+// Softmax reference.  The weights that enter the MMA are 2^(s - ref) vs: the
+// reference follows the scores plus the exponent of the V scale, so that blocks
+// of small values keep their bits where they carry the result.  The sum of the
+// weights, FP32, uses the same reference without the V scale.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -69,34 +69,37 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
 // ---------------------------------------------------------------------------
 constexpr int kQdTile = 16;       // blocks per tile
 constexpr int kQdStages = 2;      // of K and of V
-constexpr int kQdMeta = 4;        // tiles whose scales and masks are held
+constexpr int kQdMeta = 8;        // tiles whose scales and masks are held
 constexpr int kQdThreads = 384;   // K and V producers, QK and PV issuers, 8 softmax warps
-constexpr int kQdCols = 128;      // TMEM: S 2 x 32, O 2 x 32
+constexpr int kQdS = 4;           // score buffers: the QK issuer runs ahead, so that K stages are free early
+constexpr int kQdCols = 256;      // TMEM: S 4 x 32, O 2 x 32
 constexpr int kQdMaxSplit = 8;    // splits of a row = one (portable) cluster
 constexpr int kQdStage = kQdTile * kQ8Half;  // bytes of a stage
 
-struct __align__(1024) QdSmem {
+struct __align__(512) QdSmem {
   uint8_t k[kQdStages][kQdTile][3][8][64];    // [block][chunk of 64 dims][8 rows][64 B], 64-byte swizzle
   uint8_t v[kQdStages][kQdTile][3][8][64];
   uint8_t q[3][32][64];                       // [chunk][16 hi, 16 lo][64 B], 64-byte swizzle
   uint8_t p[2][kQdTile * kQ8Tok][32];         // [token][16 hi, 16 lo], 32-byte swizzle
-  float4 meta[kQdMeta][kQdTile];              // a tile's blocks: K scale, V scale, its log2, attended tokens (bits)
+  float2 scale[kQdMeta][kQdTile];             // a tile's blocks: K scale, V scale
+  int32_t mask[kQdMeta][kQdTile];             // attended tokens (bits 0-7), floor(log2(V scale)) above them
   float wmax[4][kHg];                         // a reference change: maxima of the four lane quadrants
   float qscale[kHg];
   uint64_t k_full[kQdStages], k_empty[kQdStages], v_full[kQdStages], v_empty[kQdStages], meta_full[kQdMeta];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, o_final, drain[2];
+  uint64_t s_full[kQdS], s_free[kQdS], p_full[2], pv_done[2], q_full, o_final, drain[2];
   uint32_t tmem;
   int abort;
 };
 
+constexpr int kQdOStride = kD + 2;
 // The combine's view of the K ring, once the last MMA is done.
 struct QdOut {
-  float m[kHg], l[kHg];            // this split's reference and sum
-  float f[kQdMaxSplit][kHg];       // factor of every split
+  float m[kHg];                    // this split's reference
+  float f[kQdMaxSplit][kHg], lr[kQdMaxSplit][kHg];  // every split's, then its factor
   float fin[kHg], wfac[kHg];       // normalisation (and gate); weight normalisation
   float mu[kHg];                   // the splits' common reference
-  float wl[4][kHg];
-  float o[kHg][kD + 1];
+  float wl[4][kHg];                // and its sums by lane quadrant
+  float o[kHg][kQdOStride];
 };
 static_assert(sizeof(QdOut) <= kQdStages * kQdStage, "the combine fits the K ring");
 
@@ -117,7 +120,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
                       __nv_bfloat16* __restrict__ out, QdWeights wts, int64_t nq, int G, int k, int64_t q_pos0,
                       int64_t blocks, int nsplit, float scale_log2) {
   extern __shared__ uint8_t smem_raw[];
-  QdSmem& sm = *reinterpret_cast<QdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  QdSmem& sm = *reinterpret_cast<QdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~static_cast<uintptr_t>(511));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % nsplit;
   const int64_t row = blockIdx.x / nsplit;  // (seq * nq + i) * G + g
@@ -151,9 +154,11 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       tc::mbar_init(bar(sm.v_empty[s]), 1);
     }
     for (int s = 0; s < kQdMeta; ++s) tc::mbar_init(bar(sm.meta_full[s]), kQdTile);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kQdS; ++b) {
       tc::mbar_init(bar(sm.s_full[b]), 1);
       tc::mbar_init(bar(sm.s_free[b]), 256);
+    }
+    for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(sm.p_full[b]), 256);
       tc::mbar_init(bar(sm.pv_done[b]), 1);
       tc::mbar_init(bar(sm.drain[b]), 1);
@@ -177,10 +182,20 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     fetch(1, id2, prev2);
     cnt = min(max(__ldg(sel_count + row), 0), k);
   }
+  // the softmax warps' queries: a warp packs two heads, a lane dims 2 lane and
+  // 2 lane + 1 of every chunk
+  uint32_t qw[2][3];
+  const int qh = 2 * (warp - 2);
+  if (warp >= 2 && warp <= 9) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int c = 0; c < 3; ++c) qw[hh][c] = __ldg(reinterpret_cast<const uint32_t*>(q + (row * kHg + qh + hh) * kD) + 32 * c + lane);
+  }
   if (warp == 1) tc::tmem_alloc(smem_u32(&sm.tmem), kQdCols);
   __syncthreads();
   tc::fence_after();
-  const uint32_t tS = sm.tmem, tO = sm.tmem + 64;
+  const uint32_t tS = sm.tmem, tO = sm.tmem + 32 * kQdS;
   int issued = 0;  // producers: tiles whose copies this warp issued
 
   // per-head state of the softmax threads
@@ -214,8 +229,10 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
         tc::tma_load_5d(smem_u32(is_k ? &sm.k[s][lane][0][0][0] : &sm.v[s][lane][0][0][0]), &kvmap, 0, is_k ? 0 : kQ8Tok, 0,
                         blk >= 0 ? g : 0, blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
         if (is_k) {
-          const uint32_t m = blk < 0 ? 0u : blk == hist ? (2u << (t % kQ8Tok)) - 1u : 0xFFu;
-          sm.meta[j % kQdMeta][lane] = make_float4(sc.x, m != 0 ? sc.y : 0.f, m != 0 ? log2f(sc.y) : 0.f, __uint_as_float(m));
+          const int32_t m = blk < 0 ? 0 : blk == hist ? (2 << (t % kQ8Tok)) - 1 : 0xFF;
+          const int32_t e = blk < 0 || !isfinite(sc.y) ? 0 : static_cast<int32_t>(__float_as_uint(sc.y) >> 23) - 127;
+          sm.scale[j % kQdMeta][lane] = make_float2(sc.x, blk < 0 ? 0.f : sc.y);
+          sm.mask[j % kQdMeta][lane] = e * 256 + m;
           tc::mbar_arrive(bar(sm.meta_full[j % kQdMeta]));
         }
       }
@@ -232,9 +249,9 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     const uint64_t dq0 = tc::sdesc(smem_u32(&sm.q[0][0][0]), 16, 512, tc::kSw64);
     bool ok = tc::warp_wait(bar(sm.q_full), 0, abort);
     for (int j = 0; ok && j < n_tiles; ++j) {
-      const int s = j % kQdStages, b = j & 1;
+      const int s = j % kQdStages, b = j % kQdS;
       ok = tc::warp_wait(bar(sm.k_full[s]), (j / kQdStages) & 1, abort);
-      if (ok && j >= 2) ok = tc::warp_wait(bar(sm.s_free[b]), ((j >> 1) - 1) & 1, abort);
+      if (ok && j >= kQdS) ok = tc::warp_wait(bar(sm.s_free[b]), ((j / kQdS) - 1) & 1, abort);
       if (!ok) break;
       tc::fence_after();
       if (tc::elect_one()) {
@@ -283,16 +300,14 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     const int sw = warp - 2, quad = warp & 3, half = sw >> 2, h0 = 8 * half, hbar = 1 + half;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const int tok = quad * 32 + lane;  // token of the tile = TMEM lane
-    // queries: a warp packs two heads, a lane dims 2 lane, 2 lane + 1 of every chunk
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
-      const int h = h0 + 2 * (sw & 3) + hh;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(q + (row * kHg + h) * kD);
+      const int h = qh + hh;
       float x[3][2], mx = 0.f;
       bool fin = true;
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        const uint32_t w = src[32 * c + lane];
+        const uint32_t w = qw[hh][c];
         x[c][0] = __uint_as_float(w << 16);
         x[c][1] = __uint_as_float(w & 0xFFFF0000u);
         fin = fin && isfinite(x[c][0]) && isfinite(x[c][1]);
@@ -320,25 +335,27 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     for (int h = 0; h < 8; ++h) rc[h] = sm.qscale[h0 + h];
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      const int b = j & 1;
+      const int b = j & 1, sb = j % kQdS;
       ok = ok && tc::mbar_wait(bar(sm.meta_full[j % kQdMeta]), (j / kQdMeta) & 1, abort);
-      const float4 meta = sm.meta[j % kQdMeta][tok >> 3];
-      const bool use = (__float_as_uint(meta.w) >> (tok & 7)) & 1u;
-      ok = ok && tc::mbar_wait(bar(sm.s_full[b]), (j >> 1) & 1, abort);
+      const float2 sc = sm.scale[j % kQdMeta][tok >> 3];
+      const int32_t msk = sm.mask[j % kQdMeta][tok >> 3];
+      const bool use = (msk >> (tok & 7)) & 1;
+      const float lvs = static_cast<float>(msk >> 8);
+      ok = ok && tc::mbar_wait(bar(sm.s_full[sb]), (j / kQdS) & 1, abort);
       tc::fence_after();
       uint32_t sh[8], sl[8];
-      tc::tmem_ld8(tS + 32 * b + lane_off + h0, sh);
-      tc::tmem_ld8(tS + 32 * b + lane_off + 16 + h0, sl);
+      tc::tmem_ld8(tS + 32 * sb + lane_off + h0, sh);
+      tc::tmem_ld8(tS + 32 * sb + lane_off + 16 + h0, sl);
       tc::tmem_ld_wait();
       tc::fence_before();
-      tc::mbar_arrive(bar(sm.s_free[b]));
+      tc::mbar_arrive(bar(sm.s_free[sb]));
       float x[8];
       bool grow = false;
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        const float v = fmaf(__uint_as_float(sl[h]), 0.0625f, __uint_as_float(sh[h])) * (meta.x * rc[h]);
+        const float v = fmaf(__uint_as_float(sl[h]), 0.0625f, __uint_as_float(sh[h])) * (sc.x * rc[h]);
         x[h] = use ? v : -INFINITY;
-        grow = grow || x[h] + meta.z > ref[h] + 8.f;
+        grow = grow || x[h] + lvs > ref[h] + 8.f;
       }
       // does any weight of the tile exceed 2^8?
       int any;
@@ -352,7 +369,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
         // the largest weights stay between 2^4 and 2^8
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
-          const int v = __float_as_int(fmaxf(x[h] + meta.z, -INFINITY));
+          const int v = __float_as_int(fmaxf(x[h] + lvs, -INFINITY));
           const int mx = __reduce_max_sync(0xffffffffu, v ^ ((v >> 31) & 0x7FFFFFFF));
           if (lane == 0) sm.wmax[quad][h0 + h] = __int_as_float(mx ^ ((mx >> 31) & 0x7FFFFFFF));
         }
@@ -391,7 +408,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           l[h + e] += x[h + e];
         }
         uint32_t a, c;
-        split_e4m3(x[h] * meta.y, x[h + 1] * meta.y, a, c, 16.f);
+        split_e4m3(x[h] * sc.y, x[h + 1] * sc.y, a, c, 16.f);
         if (h & 2) {
           hi[h >> 2] |= a << 16;
           lo[h >> 2] |= c << 16;
@@ -429,6 +446,12 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           for (int h = 0; h < 8; ++h) r[h] = ref[h];
         }
       }
+    }
+    // the threads' sums, while the last product runs (the wait below covers it)
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
     }
     if (n_tiles > 0) ok = ok && tc::mbar_wait(bar(sm.o_final), 0, abort);
   }
@@ -468,55 +491,73 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
         for (int h = 0; h < 8; ++h) po.o[h0 + h][64 + d] = fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h]));
       }
     } else {
-      for (int x = threadIdx.x - 64; x < kHg * (kD + 1); x += 256) (&po.o[0][0])[x] = 0.f;
+      for (int x = threadIdx.x - 64; x < kHg * kQdOStride; x += 256) (&po.o[0][0])[x] = 0.f;
     }
+    if (lane == 0) {
 #pragma unroll
-    for (int h = 0; h < 8; ++h) {
-      float v = l[h];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) po.wl[quad][h0 + h] = v;
-      if (quad == 0 && lane == 0) po.m[h0 + h] = ref[h];
+      for (int h = 0; h < 8; ++h) {
+        po.wl[quad][h0 + h] = l[h];
+        if (quad == 0) po.m[h0 + h] = ref[h];
+      }
     }
     tc::fence_before();
   }
-  __syncthreads();
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
   if (warp == 1) {
     tc::fence_after();
     tc::tmem_dealloc(sm.tmem, kQdCols);
   }
-  if (threadIdx.x < kHg)
-    po.l[threadIdx.x] = (po.wl[0][threadIdx.x] + po.wl[1][threadIdx.x]) + (po.wl[2][threadIdx.x] + po.wl[3][threadIdx.x]);
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
+  // This split finalises pairs [split * n, split * n + n) of the row's 16 x 96
+  // pairs of outputs.  Every remote read of a step is issued before the first
+  // is used: one trip through the cluster for the references, one for O.
+  const int n = (kHg * kD / 2 + nsplit - 1) / nsplit;
+  const int i1 = min(kHg * kD / 2, split * n + n);
+  float2 part[kQdMaxSplit];
+  auto read_parts = [&](int x) {
+    const int h = x / (kD / 2), d = 2 * (x - h * (kD / 2));
+#pragma unroll
+    for (int r = 0; r < kQdMaxSplit; ++r)
+      if (r < nsplit) part[r] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(&po.o[h][d], r));
+  };
+  if (static_cast<int>(threadIdx.x) < nsplit * kHg) {
+    const int r = threadIdx.x / kHg, h = threadIdx.x % kHg;
+    const QdOut* other = cluster.map_shared_rank(&po, r);
+    const float m = other->m[h], w0 = other->wl[0][h], w1 = other->wl[1][h], w2 = other->wl[2][h], w3 = other->wl[3][h];
+    po.f[r][h] = m;
+    po.lr[r][h] = (w0 + w1) + (w2 + w3);
+  }
+  const int x0 = split * n + threadIdx.x;
+  if (x0 < i1) read_parts(x0);
+  __syncthreads();
   if (threadIdx.x < kHg) {
     const int h = threadIdx.x;
     float mm = -INFINITY;
-    for (int r = 0; r < nsplit; ++r) mm = fmaxf(mm, cluster.map_shared_rank(po.m, r)[h]);
+    for (int r = 0; r < nsplit; ++r) mm = fmaxf(mm, po.f[r][h]);
     const float mu = mm == -INFINITY ? 0.f : mm;
     float ls = 0.f;
     for (int r = 0; r < nsplit; ++r) {
-      const float lr = cluster.map_shared_rank(po.l, r)[h];
-      const float a = exp2f(cluster.map_shared_rank(po.m, r)[h] - mu);
+      const float a = exp2f(po.f[r][h] - mu);
       po.f[r][h] = a;
-      ls += lr == 0.f ? 0.f : a * lr;
+      ls += po.lr[r][h] == 0.f ? 0.f : a * po.lr[r][h];
     }
     po.fin[h] = gate_factor(gate, row * kHg + h) / ls;
     po.wfac[h] = 1.f / ls;  // a weight sum with reference r counts 2^(r - mu) / ls
     po.mu[h] = mu;
   }
   __syncthreads();
-  {
-    // this split finalises outputs [split * n, split * n + n) of the row's 16 x 192
-    const int n = (kHg * kD + nsplit - 1) / nsplit;
-    const int i0 = split * n, i1 = min(kHg * kD, i0 + n);
-    for (int x = i0 + threadIdx.x; x < i1; x += kQdThreads) {
-      const int h = x / kD, d = x - h * kD;
-      float a = 0.f;
-      for (int r = 0; r < nsplit; ++r) a = fmaf(po.f[r][h], cluster.map_shared_rank(&po.o[0][0], r)[h * (kD + 1) + d], a);
-      out[row * kHg * kD + x] = __float2bfloat16_rn(a * po.fin[h]);
-    }
+  for (int x = x0; x < i1; x += kQdThreads) {
+    if (x != x0) read_parts(x);
+    const int h = x / (kD / 2);
+    float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kQdMaxSplit; ++r)
+      if (r < nsplit) {
+        a.x = fmaf(po.f[r][h], part[r].x, a.x);
+        a.y = fmaf(po.f[r][h], part[r].y, a.y);
+      }
+    reinterpret_cast<uint32_t*>(out)[row * (kHg * kD / 2) + x] = pack_bf16x2(a.x * po.fin[h], a.y * po.fin[h]);
   }
   if (WEIGHTS) {
     const int n_cnt = min(max(sel_count[row], 0), k);

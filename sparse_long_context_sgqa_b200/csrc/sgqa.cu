@@ -726,8 +726,8 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
       wt.refs = ws_at<float>(ws, w.refs_off);
       wt.tiles = nsplit * ((per + sgqa::kQdTile - 1) / sgqa::kQdTile);
     }
-    static_assert(2 * (sizeof(sgqa::QdSmem) + 2048) <= 233472, "two CTAs per SM");
-    const size_t smem = sizeof(sgqa::QdSmem) + 1024;
+    static_assert(2 * (sizeof(sgqa::QdSmem) + 512 + 1024) <= 233472, "two CTAs per SM");
+    const size_t smem = sizeof(sgqa::QdSmem) + 512;
     auto kern = acc != nullptr ? sgqa::attn_q8_decode_kernel<true> : sgqa::attn_q8_decode_kernel<false>;
     cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     cudaLaunchConfig_t cfg = {};

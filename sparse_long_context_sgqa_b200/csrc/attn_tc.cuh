@@ -495,7 +495,10 @@ attn_tc_kernel(const __nv_bfloat16* __restrict__ q, const __grid_constant__ CUte
       sm.mchain[m] = m_use;
       if (j + 1 < n_tiles) asm volatile("bar.arrive %0, 64;" ::"r"(pub_mine) : "memory");
       if (__any_sync(0xffffffffu, need)) {
-        // O must hold P(j-1) V(j-1) before it is rescaled
+        // O must hold P(j-1) V(j-1) before it is rescaled.  This warp has seen no
+        // phase of that barrier yet: a wait for the phase of tile j-1 means what it
+        // says only once the phase of tile j-3 is over, which tile j-2's product shows.
+        if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j / 2) - 1) & 1, abort);
         ok = ok && tc::mbar_wait(bar(sm.pv_done[(j - 1) % 2]), ((j - 1) / 2) & 1, abort);
         tc::fence_after();
         const float alpha = need ? exp2f(m_prev - m_use) : 1.f;

@@ -571,12 +571,547 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 #pragma unroll
       for (int h = 0; h < kHg; ++h) {
         const float v = ws[h];
-        w += v == 0.f ? 0.f : v * exp2f((rs[h] == -INFINITY ? 0.f : rs[h]) - po.mu[h]) * po.wfac[h];
+        const float u = v == 0.f ? 0.f : v * exp2f((rs[h] == -INFINITY ? 0.f : rs[h]) - po.mu[h]) * po.wfac[h];
+        w += u == u ? u : 0.f;  // NaN: not counted
       }
       acc_add(wts.acc + seq * blocks + blk, w);
     }
   }
   cluster.sync();  // no split leaves while others still read its shared memory
+}
+
+// ---------------------------------------------------------------------------
+// Many queries (prefill).  The unit and the union of its queries' blocks are
+// those of attn_tc_kernel (attn_tc.cuh): 8 adjacent queries x 16 heads = the 128 MMA rows, 64-token tiles of the union, then a
+// tile with the current blocks.  What differs is the operands:
+//   S = Q K^T   2 x 6 MMAs (E4M3, M128 N64 K32): Q's hi and lo halves from TMEM,
+//               K's codes as gathered.  Twice the passes at twice the BF16 rate.
+//   O += P V    4 MMAs (FP16, M128 N192 K16): P from TMEM, V's codes widened to
+//               FP16 (exact) in shared memory by a warpgroup of its own.  P needs the
+//               range of 16 bits: where one token takes most of a row (a sink), the
+//               result lies in weights 2^-14 of the largest and below, which two
+//               E4M3 halves in one accumulator lose.
+// lo is not multiplied by 16 here (both halves add into one accumulator): it
+// resolves 2^-10 below a row's largest query value of 224 .. 448.
+// A block's K scale and the row's query scale multiply its scores; its V scale
+// enters the exponent (2^(s + log2 vs - ref)) and leaves the block's sum again.
+//
+// WEIGHTS: the second sweep of a call that accumulates weights.  With every
+// row's log-sum known, S alone is computed again, the halves in buffers of
+// their own (lo times 16), and each block's weights are summed over the unit's
+// 128 rows, eight blocks of a tile at a time.
+// ---------------------------------------------------------------------------
+constexpr int kQpStages = 8;      // K ring depth, 12 KB each
+constexpr int kQpVStages = 4;     // V ring depth (codes)
+constexpr int kQpThreads = 512;   // producers and issuers, V widening, 2 x softmax: a warpgroup each
+constexpr int kQpTile = 8;        // blocks per tile
+constexpr int kQpMeta = 4;        // batches (of 4 tiles) whose scales are held
+
+struct __align__(1024) QpSmem {
+  uint8_t v16[2][kQpTile][3][1024];          // widened V: [block][chunk][8 rows x 128 B], 128-byte swizzle
+  uint8_t k[kQpStages][kQpTile][3][8][64];   // [block][chunk][8 rows][64 B], 64-byte swizzle
+  uint8_t v[kQpVStages][kQpTile][3][8][64];
+  float4 meta[kQpMeta][32];                 // per block: K scale, log2(V scale), 1 / V scale, V scale finite (1) or not (0)
+  float4 meta_cur[8];                       // of the current blocks (two are used)
+  int32_t ids[kQpMeta][32];                 // WEIGHTS: the blocks
+  uint64_t q_full;
+  uint64_t k_full[kQpStages], k_empty[kQpStages], v_full[kQpVStages], v_empty[kQpVStages], meta_full[kQpMeta];
+  uint64_t w_full[2], w_empty[2];           // widened V
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t o_final, drain, drain_pv;
+  float pmax[2][2][128];                    // per tile parity and warp of a pair: the rows' largest score
+  float lsum[2][128];                       // partial row sums of the two warps of a pair
+  float gfac[128];
+  uint32_t tmem;
+  int abort;
+};
+
+template <bool WEIGHTS, bool SKIP_PAIRS>
+__global__ void __launch_bounds__(kQpThreads, 1)
+attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfloat16* __restrict__ q,
+                       const float* __restrict__ kv_scale, const int32_t* __restrict__ plan_ids,
+                       const uint8_t* __restrict__ plan_mask, const int32_t* __restrict__ plan_count,
+                       const __nv_bfloat16* __restrict__ gate, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+                       int64_t* __restrict__ acc, int64_t nq, int G, int k, int64_t q_pos0, int64_t blocks,
+                       float scale_log2) {
+  extern __shared__ uint8_t smem_raw[];
+  QpSmem& sm = *reinterpret_cast<QpSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // group-major order: CTAs resident together read one group's K/V (L2 reuse)
+  const int64_t nqb = (nq + 7) / 8;
+  const int64_t per_group = static_cast<int64_t>(gridDim.x) / G;
+  const int g = static_cast<int>(blockIdx.x / per_group);
+  const int64_t sq = blockIdx.x % per_group;  // seq * nqb + qb
+  const int64_t qb = sq % nqb;
+  const int64_t seq = sq / nqb;
+  const int64_t unit = sq * G + g;
+  const int U = plan_count[unit];
+  const int32_t* uid = plan_ids + unit * (8 * static_cast<int64_t>(k));
+  const uint8_t* umask = plan_mask + unit * (8 * static_cast<int64_t>(k));
+  const int n_union_tiles = (U + kQpTile - 1) / kQpTile;
+  const int n_tiles = n_union_tiles + 1;
+  const int64_t t_first = q_pos0 + qb * 8;
+  const int64_t t_last = q_pos0 + min(nq, qb * 8 + 8) - 1;
+  const int64_t cb = t_first / 8;  // the first query's current block
+  const int64_t c0 = 8 * cb;
+  volatile int* abort = &sm.abort;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    tc::mbar_init(bar(sm.q_full), 256);
+    for (int s = 0; s < kQpStages; ++s) {
+      tc::mbar_init(bar(sm.k_full[s]), 1);
+      tc::mbar_init(bar(sm.k_empty[s]), 1);
+    }
+    for (int s = 0; s < kQpVStages; ++s) {
+      tc::mbar_init(bar(sm.v_full[s]), 1);
+      tc::mbar_init(bar(sm.v_empty[s]), 128);
+    }
+    for (int b = 0; b < kQpMeta; ++b) tc::mbar_init(bar(sm.meta_full[b]), 32);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(bar(sm.s_full[b]), 1);
+      tc::mbar_init(bar(sm.s_free[b]), 256);
+      tc::mbar_init(bar(sm.p_full[b]), 256);
+      tc::mbar_init(bar(sm.pv_done[b]), 1);
+      tc::mbar_init(bar(sm.w_full[b]), 128);
+      tc::mbar_init(bar(sm.w_empty[b]), 1);
+    }
+    tc::mbar_init(bar(sm.o_final), 1);
+    tc::mbar_init(bar(sm.drain), 1);
+    tc::mbar_init(bar(sm.drain_pv), 1);
+    tc::mbar_fence_init();
+  }
+  if (warp == 1) tc::tmem_alloc(smem_u32(&sm.tmem), 512);
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem;
+  const uint32_t tO = tmem;                              // columns [0, 192)
+  const uint32_t tS0 = WEIGHTS ? tmem : tmem + 192;      // S buffers: 64 columns each; WEIGHTS: hi 64, lo 64
+  constexpr uint32_t kSBuf = WEIGHTS ? 128 : 64;
+  const uint32_t tP0 = tmem + 320;                       // P buffers [320, 352), [352, 384), two FP16 per column
+  const uint32_t tQ = tmem + 384;                        // Q: hi [384, 432), lo [432, 480)
+  int issued = 0;
+
+  if (warp < 4) {
+    if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------------- producers
+      const bool is_k = warp == 0;
+      if (tc::elect_one()) tc::prefetch_tmap(&kvmap);
+      __syncwarp();
+      // Union blocks one per lane in batches of four tiles, fetched a whole batch
+      // ahead; lane 8 t + e holds block e of tile 4 b + t (-1: a zero-filled box).
+      auto load_batch = [&](int bt) -> int32_t {
+        const int idx = 32 * bt + lane;
+        return idx < U ? uid[idx] : -1;
+      };
+      auto scales = [&](int64_t blk) -> float4 {
+        if (blk < 0) return make_float4(0.f, 0.f, 1.f, 1.f);
+        const float2 s = __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g);
+        const bool fin = s.y == s.y;
+        return make_float4(s.x, fin ? log2f(s.y) : 0.f, fin ? 1.f / s.y : 1.f, fin ? 1.f : 0.f);
+      };
+      if (!WEIGHTS || is_k) {
+        int32_t ids_cur = load_batch(0), ids_next = n_union_tiles > 4 ? load_batch(1) : -1;
+        float4 sc_next = make_float4(0.f, 0.f, 1.f, 1.f);
+        if (is_k) {
+          if (lane < 8) sm.meta_cur[lane] = scales(lane == 0 || (lane == 1 && c0 + 8 <= t_last) ? cb + lane : -1);
+          sm.meta[0][lane] = scales(ids_cur);
+          sm.ids[0][lane] = ids_cur;
+          tc::mbar_arrive(bar(sm.meta_full[0]));
+          sc_next = scales(ids_next);
+        }
+        for (int j = 0; j < n_tiles; ++j) {
+          const int nst = is_k ? kQpStages : kQpVStages;
+          const int s = j % nst;
+          if (j > 0 && (j & 3) == 0) {
+            const int bt = j / 4;
+            ids_cur = ids_next;
+            if (is_k && j < n_union_tiles) {
+              // Batch bt - 4 was read: this stage's last QK (tile j - 8) waited for the
+              // score buffer of tile j - 10, which the softmax frees after its scales.
+              if (j >= kQpStages && !tc::warp_wait(bar(sm.k_empty[s]), ((j / kQpStages) - 1) & 1, abort)) break;
+              sm.meta[bt % kQpMeta][lane] = sc_next;
+              sm.ids[bt % kQpMeta][lane] = ids_cur;
+              tc::mbar_arrive(bar(sm.meta_full[bt % kQpMeta]));
+            }
+            ids_next = 4 * (bt + 1) < n_union_tiles ? load_batch(bt + 1) : -1;
+            if (is_k) sc_next = scales(ids_next);
+          }
+          int32_t blk[kQpTile];
+#pragma unroll
+          for (int e = 0; e < kQpTile; ++e) {
+            const int32_t id = __shfl_sync(0xffffffffu, ids_cur, 8 * (j & 3) + e);
+            if (j < n_union_tiles) blk[e] = id;
+            else blk[e] = (e == 0 || (e == 1 && c0 + 8 <= t_last)) ? static_cast<int32_t>(cb) + e : -1;
+          }
+          if (j >= nst && !tc::warp_wait(bar(is_k ? sm.k_empty[s] : sm.v_empty[s]), ((j / nst) - 1) & 1, abort)) break;
+          if (tc::elect_one()) {
+            const uint32_t full = bar(is_k ? sm.k_full[s] : sm.v_full[s]);
+            tc::mbar_expect_tx(full, kQpTile * kQ8Half);
+            const uint32_t dst = smem_u32(is_k ? &sm.k[s][0][0][0][0] : &sm.v[s][0][0][0][0]);
+#pragma unroll
+            for (int e = 0; e < kQpTile; ++e)
+              tc::tma_load_5d(dst + e * kQ8Half, &kvmap, 0, is_k ? 0 : kQ8Tok, 0, blk[e] >= 0 ? g : 0,
+                              blk[e] >= 0 ? static_cast<int32_t>(seq * blocks + blk[e]) : -1, full);
+          }
+          __syncwarp();
+          issued = j + 1;
+        }
+      }
+    } else if (warp == 1 || warp == 3) {
+      // ---------------------------------------------------------------- MMA issuers
+      const uint32_t id_qk = tc::idesc_e4m3(128, 64, false, false);
+      const uint32_t id_pv = tc::idesc_f16(128, 192, true);
+      const uint64_t dk0 = tc::sdesc(smem_u32(&sm.k[0][0][0][0][0]), 16, kQ8Half, tc::kSw64);
+      const uint64_t dv0 = tc::sdesc_sw128(smem_u32(&sm.v16[0][0][0][0]), 1024, 2 * kQ8Half);
+      constexpr uint32_t kStage = kQpTile * kQ8Half / 16;
+      bool ok = true;
+      if (warp == 1) {
+        ok = tc::warp_wait(bar(sm.q_full), 0, abort);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const int s = j % kQpStages, b = j % 2;
+          ok = tc::warp_wait(bar(sm.k_full[s]), (j / kQpStages) & 1, abort);
+          if (ok && j >= 2) ok = tc::warp_wait(bar(sm.s_free[b]), ((j / 2) - 1) & 1, abort);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t dk = dk0 + kStage * s;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int kk = 0; kk < 6; ++kk)  // Q: 8 columns per 32 dims; K: +512 B per 64 dims, +32 B per 32
+                tc::mma_f8_tmem_a(tS0 + kSBuf * b + (WEIGHTS ? 64 * half : 0), tQ + 48 * half + 8 * kk,
+                                  dk + (kk >> 1) * 32 + (kk & 1) * 2, id_qk, (kk > 0 || (!WEIGHTS && half > 0)) ? 1u : 0u);
+            tc::mma_commit(bar(sm.k_empty[s]));
+            tc::mma_commit(bar(sm.s_full[b]));
+          }
+          __syncwarp();
+        }
+      } else if (!WEIGHTS) {
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const int b = j % 2;
+          ok = tc::warp_wait(bar(sm.w_full[b]), (j / 2) & 1, abort) && tc::warp_wait(bar(sm.p_full[b]), (j / 2) & 1, abort);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t dv = dv0 + 2 * kStage * b;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 16 tokens: V +2 blocks, P +8 columns
+              tc::mma_f16_tmem_a(tO, tP0 + 32 * b + 8 * kk, dv + (4 * kQ8Half / 16) * kk, id_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_commit(bar(sm.w_empty[b]));
+            tc::mma_commit(bar(sm.pv_done[b]));
+          }
+          __syncwarp();
+        }
+        if (ok) {
+          if (tc::elect_one()) tc::mma_commit(bar(sm.o_final));
+          __syncwarp();
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- V codes -> FP16
+    // A warp takes six of a tile's 24 (block, chunk) pieces, a lane one 16-byte
+    // piece of a row in each: 512 contiguous bytes in, two conflict-free 16-byte
+    // stores per lane out.
+    if (!WEIGHTS) {
+      const uint32_t r = lane >> 2, c = lane & 3;
+      const uint32_t src_off = sw64_offset(r, 16 * c);
+      const uint32_t dst0 = r * 128 + (((2 * c) ^ r) << 4), dst1 = r * 128 + (((2 * c + 1) ^ r) << 4);
+      bool ok = true;
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int s = j % kQpVStages, b = j % 2;
+        ok = tc::warp_wait(bar(sm.v_full[s]), (j / kQpVStages) & 1, abort);
+        if (ok && j >= 2) ok = tc::warp_wait(bar(sm.w_empty[b]), ((j / 2) - 1) & 1, abort);
+        if (!ok) break;
+        const uint8_t* src = &sm.v[s][0][0][0][0] + src_off;
+        uint8_t* dst = &sm.v16[b][0][0][0];
+        uint4 x[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (6 * (warp - 4) + i) * 512);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const __half2 lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[y] & 0xFFFFu), __NV_E4M3);
+            const __half2 hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[y] >> 16), __NV_E4M3);
+            o[2 * y] = *reinterpret_cast<const uint32_t*>(&lo);
+            o[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+          }
+          uint8_t* d = dst + (6 * (warp - 4) + i) * 1024;
+          *reinterpret_cast<uint4*>(d + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(bar(sm.v_empty[s]));
+        tc::mbar_arrive(bar(sm.w_full[b]));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax + epilogue
+    // Two warps per TMEM lane quadrant share every tile: warp `half` takes blocks
+    // 4 half .. 4 half + 3 of its 32 rows.  (Half the registers and code of a whole
+    // tile per warp: with 64 columns unrolled the instruction cache missed on every
+    // tile.)  The two exchange their maxima through shared memory.  A failed wait
+    // clears `ok` but keeps every barrier step in place.
+    const int quad = warp & 3, half = (warp - 8) >> 2;
+    const int pair_bar = 1 + quad;
+    const int m = quad * 32 + lane;  // TMEM lane = row = (query slot, head)
+    const int qs = m >> 4;
+    const int64_t qi = qb * 8 + qs;
+    const bool qvalid = qi < nq;
+    const int64_t t = q_pos0 + (qvalid ? qi : qb * 8);
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const int64_t orow_idx = ((seq * nq + (qvalid ? qi : 0)) * G + g) * kHg + (m & 15);
+    if (!WEIGHTS && half == 0) sm.gfac[m] = gate_factor(gate, orow_idx);
+    // Q row m, dims [96 half, 96 half + 96): the row's scale, then codes into TMEM
+    float rc;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(q + orow_idx * kD + 96 * half);
+      uint32_t w[48];
+#pragma unroll
+      for (int c = 0; c < 12; ++c) {
+        const uint4 x = qvalid ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * c] = x.x;
+        w[4 * c + 1] = x.y;
+        w[4 * c + 2] = x.z;
+        w[4 * c + 3] = x.w;
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < 48; ++c) top = __vmaxu2(top, w[c] & 0x7FFF7FFFu);
+      top = max(top & 0xFFFFu, top >> 16);  // BF16 bits of the largest magnitude
+      sm.lsum[half][m] = __uint_as_float(top << 16);
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      const uint32_t t2 = max(__float_as_uint(sm.lsum[0][m]), __float_as_uint(sm.lsum[1][m]));
+      const bool fin = t2 < 0x7F800000u;
+      const int e = fin ? e4m3_exp(__uint_as_float(t2)) : 0;
+      const float inv = pow2f(-e);
+      rc = fin ? pow2f(e) * scale_log2 : __uint_as_float(0x7FC00000u);  // infinity or NaN: every score NaN
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        uint32_t h8[8], l8[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t a = w[16 * c + 2 * x], b = w[16 * c + 2 * x + 1];
+          uint32_t ha, la, hb, lb;
+          split_e4m3(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv, ha, la, WEIGHTS ? 16.f : 1.f);
+          split_e4m3(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv, hb, lb, WEIGHTS ? 16.f : 1.f);
+          h8[x] = ha | (hb << 16);
+          l8[x] = la | (lb << 16);
+        }
+        tc::tmem_st8(tQ + lane_off + 24 * half + 8 * c, h8);
+        tc::tmem_st8(tQ + 48 + lane_off + 24 * half + 8 * c, l8);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before();
+      tc::mbar_arrive(bar(sm.q_full));
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // lsum is reused at the end
+    }
+    float ref = -INFINITY, l = 0.f;  // the row's reference; this warp's part of the sum, relative to 2^ref
+    bool nan_v = false;              // the row attends a block whose V holds an infinity or NaN
+    const float row_lse = WEIGHTS ? (qvalid ? lse[orow_idx] : INFINITY) : 0.f;
+    bool ok = tc::mbar_wait(bar(sm.meta_full[0]), 0, abort);  // (the current blocks' scales come with it)
+    uint32_t mb_next = 0;  // mask bytes of this warp's blocks of the next tile
+    if (n_union_tiles > 0) mb_next = *reinterpret_cast<const uint32_t*>(umask + 4 * half);
+    for (int j = 0; j < n_tiles; ++j) {
+      const int b = j % 2;
+      const bool last = j >= n_union_tiles;  // the current-block tile
+      const uint32_t tS = tS0 + kSBuf * b + 32 * half + lane_off;
+      const uint32_t mb = mb_next;
+      if (j + 1 < n_union_tiles) mb_next = *reinterpret_cast<const uint32_t*>(umask + 8 * (j + 1) + 4 * half);
+      // bit e: the row's query attends this warp's block e
+      uint32_t bmask;
+      const float4* meta;
+      if (!last) {
+        bmask = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * j + 4 * half + e < U) bmask |= ((mb >> (8 * e + qs)) & 1u) << e;
+        ok = ok && tc::mbar_wait(bar(sm.meta_full[(j / 4) % kQpMeta]), (j / (4 * kQpMeta)) & 1, abort);
+        meta = &sm.meta[(j / 4) % kQpMeta][8 * (j & 3) + 4 * half];
+      } else {
+        bmask = half == 0 ? 1u << (t / 8 - cb) : 0u;
+        meta = &sm.meta_cur[4 * half];
+      }
+      // per block: the score factor, log2 and inverse of the V scale; a block the
+      // row does not attend has factor 0 and offset -inf
+      float cf[4], lv[4], iv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 mt = meta[e];
+        const bool use = (bmask >> e) & 1u;
+        cf[e] = use ? mt.x * rc : 0.f;
+        lv[e] = use ? mt.y : -INFINITY;
+        iv[e] = use ? mt.z : 0.f;
+        nan_v = nan_v || (use && mt.w == 0.f);
+      }
+      int32_t tile_id = 0;
+      if (WEIGHTS)
+        tile_id = last ? static_cast<int32_t>(cb) + (lane & 3)
+                       : sm.ids[(j / 4) % kQpMeta][8 * (j & 3) + 4 * half + (lane & 3)];
+      ok = ok && tc::mbar_wait(bar(sm.s_full[b]), (j / 2) & 1, abort);
+      tc::fence_after();
+      uint32_t sr[32];
+      tc::tmem_ld32(tS, sr);
+      tc::tmem_ld_wait();
+      if (WEIGHTS) {
+        uint32_t lo[32];
+        tc::tmem_ld32(tS + 64, lo);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          sr[x] = __float_as_uint(fmaf(__uint_as_float(lo[x]), 0.0625f, __uint_as_float(sr[x])));
+      }
+      tc::fence_before();
+      tc::mbar_arrive(bar(sm.s_free[b]));
+      if (last && half == 0) {  // tokens of the row's current block behind t
+        const int end = static_cast<int>(t - c0);
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (x > end && ((bmask >> (x >> 3)) & 1u)) sr[x] = __float_as_uint(-INFINITY);
+      }
+      if constexpr (WEIGHTS) {
+        // weights of the row, summed by block, then over the warp's 32 rows: lane
+        // 4 i + e ends with block e
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) p[x] = fast_exp2(fmaf(__uint_as_float(sr[8 * e + x]), cf[e], -row_lse));
+          w[e] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+          if (!((bmask >> e) & 1u) || !(w[e] == w[e]) || !qvalid) w[e] = 0.f;
+        }
+        float z[2];
+        const bool h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) z[c] = (h2 ? w[2 + c] : w[c]) + __shfl_xor_sync(0xffffffffu, h2 ? w[c] : w[2 + c], 2);
+        float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane < 4 && v > 0.f) acc_add(acc + seq * blocks + tile_id, v);
+      } else {
+        float bm[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* x = reinterpret_cast<const float*>(&sr[8 * e]);
+          const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+          bm[e] = fmaf(mx, cf[e], lv[e]);
+        }
+        sm.pmax[b][half][m] = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3]));
+        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+        const float mraw = fmaxf(sm.pmax[b][0][m], sm.pmax[b][1][m]);
+        // a new reference lies 8 below the largest weight and stays until one exceeds
+        // 2^15: FP16 then holds weights down to 2^-22 of the largest in full
+        const bool need = mraw > ref + 15.f;  // (ref -inf: the first attended block)
+        if (__any_sync(0xffffffffu, need)) {
+          const float old = ref;
+          if (need) ref = mraw - 8.f;
+          const float alpha = need ? exp2f(old - ref) : 1.f;
+          l *= alpha;  // (0, or NaN, while the reference is -inf)
+          if (j > 0) {
+            // O must hold P(j-1) V(j-1) before it is rescaled; each warp of the pair takes half of its columns
+            ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);
+            tc::fence_after();
+#pragma unroll 1
+            for (int h = 3 * half; h < 3 * half + 3; ++h) {
+              uint32_t o[32];
+              tc::tmem_ld32(tO + lane_off + 32 * h, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tc::tmem_st32(tO + lane_off + 32 * h, o);
+            }
+          }
+        }
+        // P = 2^(s + log2 vs - ref)
+        const float neg = ref == -INFINITY ? 0.f : -ref;
+        uint32_t pk[16];
+        float ls = 0.f;
+        const uint32_t wmask = SKIP_PAIRS ? __reduce_or_sync(0xffffffffu, bmask) : 0xFu;
+#pragma unroll
+        for (int e2 = 0; e2 < 4; e2 += 2) {
+          if (!SKIP_PAIRS || ((wmask >> e2) & 3u)) {
+#pragma unroll
+            for (int e = e2; e < e2 + 2; ++e) {
+              const float off = lv[e] + neg;
+              float pe[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) pe[x] = fast_exp2(fmaf(__uint_as_float(sr[8 * e + x]), cf[e], off));
+              ls = fmaf(((pe[0] + pe[1]) + (pe[2] + pe[3])) + ((pe[4] + pe[5]) + (pe[6] + pe[7])), iv[e], ls);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) pk[4 * e + x] = pack_f16x2(pe[2 * x], pe[2 * x + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
+          }
+        }
+        l += ls;
+        // P buffer b is free once O += P(j-2) V(j-2) has read it
+        if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j / 2) - 1) & 1, abort);
+        tc::fence_after();
+        tc::tmem_st16(tP0 + 32 * b + 16 * half + lane_off, pk);
+        tc::tmem_st_wait();
+        tc::fence_before();
+        tc::mbar_arrive(bar(sm.p_full[b]));
+      }
+    }
+    if (!WEIGHTS) {
+      ok = ok && tc::mbar_wait(bar(sm.o_final), 0, abort);
+      if (nan_v) sm.gfac[m] = __uint_as_float(0x7FC00000u);
+      sm.lsum[half][m] = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      const float ltot = sm.lsum[0][m] + sm.lsum[1][m];
+      if (ok) {
+        tc::fence_after();
+        const float inv = sm.gfac[m] / ltot;  // softmax normalisation and output gate
+        if (lse != nullptr && half == 0 && qvalid) lse[orow_idx] = (ref == -INFINITY ? 0.f : ref) + log2f(ltot);
+        __nv_bfloat16* orow = out + orow_idx * kD;
+#pragma unroll 1
+        for (int h = 3 * half; h < 3 * half + 3; ++h) {
+          uint32_t o[32];
+          tc::tmem_ld32(tO + lane_off + 32 * h, o);
+          tc::tmem_ld_wait();
+          if (qvalid) {
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(o[8 * v4 + 0]) * inv, __uint_as_float(o[8 * v4 + 1]) * inv);
+              w.y = pack_bf16x2(__uint_as_float(o[8 * v4 + 2]) * inv, __uint_as_float(o[8 * v4 + 3]) * inv);
+              w.z = pack_bf16x2(__uint_as_float(o[8 * v4 + 4]) * inv, __uint_as_float(o[8 * v4 + 5]) * inv);
+              w.w = pack_bf16x2(__uint_as_float(o[8 * v4 + 6]) * inv, __uint_as_float(o[8 * v4 + 7]) * inv);
+              *reinterpret_cast<uint4*>(orow + 32 * h + 8 * v4) = w;
+            }
+          }
+        }
+      }
+    }
+  }
+  // The abort flag is final here; after a failed wait the copies and MMAs in
+  // flight land before shared memory and TMEM are released.
+  __syncthreads();
+  if (sm.abort) {
+    if (warp == 0 || warp == 2) {
+      const int nst = warp == 0 ? kQpStages : kQpVStages;
+      for (int j = issued > nst ? issued - nst : 0; j < issued; ++j)
+        tc::mbar_drain(bar(warp == 0 ? sm.k_full[j % nst] : sm.v_full[j % nst]), (j / nst) & 1);
+    } else if (warp == 1 || warp == 3) {
+      uint64_t& d = warp == 1 ? sm.drain : sm.drain_pv;
+      if (tc::elect_one()) tc::mma_commit(bar(d));
+      __syncwarp();
+      tc::mbar_drain(bar(d), 0);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace sgqa

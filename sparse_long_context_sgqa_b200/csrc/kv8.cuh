@@ -119,121 +119,4 @@ __device__ __forceinline__ void acc_add(int64_t* acc, float w) {
     atomicAdd(reinterpret_cast<unsigned long long*>(acc), static_cast<unsigned long long>(__float2ll_rn(w * kAccUnits)));
 }
 
-// ---------------------------------------------------------------------------
-// Attention over the cache, one CTA per (sequence, query, group): FP32 on CUDA
-// cores, 32 tokens (4 blocks) at a time; with acc a second sweep adds each
-// block's weight.
-// ---------------------------------------------------------------------------
-constexpr int kQ8SimpleThreads = 256;
-struct Q8SimpleSmem {
-  float q[kHg][kD + 1];
-  float kv[32][kD + 1];
-  float s[kHg][33];
-  float m[kHg], l[kHg], a[kHg];
-};
-
-__global__ void __launch_bounds__(kQ8SimpleThreads)
-attn_q8_simple_kernel(const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ kv8,
-                      const float* __restrict__ kv_scale, const int32_t* __restrict__ sel,
-                      const int32_t* __restrict__ sel_count, const __nv_bfloat16* __restrict__ gate,
-                      __nv_bfloat16* __restrict__ out, int64_t* __restrict__ acc, int64_t nq, int G, int k,
-                      int64_t q_pos0, int64_t blocks, float scale_log2) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Q8SimpleSmem& sm = *reinterpret_cast<Q8SimpleSmem*>(raw);
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  const int g = static_cast<int>(row % G);
-  const int64_t i = (row / G) % nq, seq = row / (G * nq);
-  const int64_t t = q_pos0 + i, hist = t / kQ8Tok;
-  const int cnt = min(max(sel_count[row], 0), k);
-  const int32_t* ids = sel + row * k;
-  const int nblk = cnt + 1;
-  for (int x = tid; x < kHg * kD; x += kQ8SimpleThreads)
-    sm.q[x / kD][x % kD] = __bfloat162float(q[row * kHg * kD + x]) * scale_log2;
-  if (tid < kHg) { sm.m[tid] = -INFINITY; sm.l[tid] = 0.f; }
-  float o[12];
-#pragma unroll
-  for (int x = 0; x < 12; ++x) o[x] = 0.f;
-  auto block_of = [&](int b) -> int64_t {  // -1: none
-    if (b >= nblk) return -1;
-    if (b == cnt) return hist;
-    const int id = ids[b];
-    if (id < 0 || id >= hist || (b > 0 && id <= ids[b - 1])) {
-      report(kDevBounds);
-      return -1;
-    }
-    return id;
-  };
-  const int sweeps = acc != nullptr ? 2 : 1;
-  for (int sweep = 0; sweep < sweeps; ++sweep) {
-    for (int b0 = 0; b0 < nblk; b0 += 4) {
-      for (int kind = 0; kind < (sweep == 0 ? 2 : 1); ++kind) {
-        __syncthreads();
-        for (int x = tid; x < 32 * kD; x += kQ8SimpleThreads) {
-          const int tk = x / kD, d = x % kD;
-          const int64_t b = block_of(b0 + tk / 8);
-          float val = 0.f;
-          if (b >= 0) {
-            const int64_t bg = (seq * blocks + b) * G + g;
-            if (8 * b + tk % 8 <= t) {
-              const __half_raw h = __nv_cvt_fp8_to_halfraw(kv8[bg * kQ8Blk + kind * kQ8Half + (tk % 8) * kD + d], __NV_E4M3);
-              val = __half2float(__half(h)) * kv_scale[2 * bg + kind];
-            }
-          }
-          sm.kv[tk][d] = val;
-        }
-        __syncthreads();
-        if (kind == 0) {
-          for (int x = tid; x < kHg * 32; x += kQ8SimpleThreads) {
-            const int h = x / 32, tk = x % 32;
-            const int64_t b = block_of(b0 + tk / 8);
-            float s = 0.f;
-            for (int d = 0; d < kD; ++d) s = fmaf(sm.q[h][d], sm.kv[tk][d], s);
-            sm.s[h][tk] = (b >= 0 && 8 * b + tk % 8 <= t) ? s : -INFINITY;
-          }
-          __syncthreads();
-          if (sweep == 0 && tid < kHg) {
-            float mx = sm.m[tid];
-            for (int tk = 0; tk < 32; ++tk) mx = fmaxf(mx, sm.s[tid][tk]);
-            const float mu = mx == -INFINITY ? 0.f : mx;
-            float l = 0.f;
-            for (int tk = 0; tk < 32; ++tk) {
-              const float p = sm.s[tid][tk] == -INFINITY ? 0.f : exp2f(sm.s[tid][tk] - mu);
-              sm.s[tid][tk] = p;
-              l += p;
-            }
-            sm.a[tid] = exp2f(sm.m[tid] - mu);
-            sm.l[tid] = sm.l[tid] * sm.a[tid] + l;
-            sm.m[tid] = mx;
-          } else if (sweep == 1 && tid < 4) {
-            const int64_t b = block_of(b0 + tid);
-            float w = 0.f;
-            if (b >= 0) {
-              for (int h = 0; h < kHg; ++h)
-                for (int tk = 8 * tid; tk < 8 * tid + 8; ++tk)
-                  if (sm.s[h][tk] != -INFINITY) w += exp2f(sm.s[h][tk] - sm.m[h]) / sm.l[h];
-              acc_add(acc + seq * blocks + b, w);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 12; ++x) {
-            const int idx = tid + kQ8SimpleThreads * x, h = idx / kD, d = idx % kD;
-            float r = o[x] * sm.a[h];
-            for (int tk = 0; tk < 32; ++tk)
-              if (sm.s[h][tk] != 0.f) r = fmaf(sm.s[h][tk], sm.kv[tk][d], r);
-            o[x] = r;
-          }
-        }
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < 12; ++x) {
-    const int idx = tid + kQ8SimpleThreads * x, h = idx / kD;
-    out[row * kHg * kD + idx] = __float2bfloat16_rn(o[x] * (gate_factor(gate, row * kHg + h) / sm.l[h]));
-  }
-}
-
 }  // namespace sgqa

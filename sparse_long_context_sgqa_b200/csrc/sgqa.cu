@@ -525,6 +525,36 @@ sgqa_status do_index(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, co
   return SGQA_OK;
 }
 
+// The union plan of every unit (8 queries of one group).
+sgqa_status launch_plan(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, const int32_t* sel,
+                        const int32_t* sel_count, int32_t* ids, uint8_t* msk, int32_t* cnt, cudaStream_t st) {
+  const int G = p->num_kv_groups, k = p->topk, B = p->block_size;
+  const int64_t units = S * ((nq + 7) / 8) * G;
+  const int64_t nbits = std::max<int64_t>((q0 + nq - 1) / B, 1);
+  const int nwords = static_cast<int>((nbits + 31) / 32);
+  // bitmap, prefix of every word (or, for wide id ranges, of every eighth), masks
+  auto plan_smem = [&](int pshift) {
+    return static_cast<size_t>(nwords) * 4 + static_cast<size_t>(((nwords - 1) >> pshift) + 2) * 4 +
+           static_cast<size_t>(k) * 8;
+  };
+  const int pshift = plan_smem(0) <= 96 * 1024 ? 0 : 3;
+  const size_t psmem = plan_smem(pshift);
+  if (psmem <= 200 * 1024) {
+    cudaFuncSetAttribute(sgqa::attn_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
+    sgqa::attn_plan_kernel<<<static_cast<unsigned>(units), sgqa::kPlanThreads, psmem, st>>>(
+        sel, sel_count, nq, G, k, nwords, pshift, q0, B, ids, msk, cnt);
+    SGQA_LAUNCH_CHECK("attn_plan_kernel");
+  } else {
+    const int pow2 = plan_pow2(k);
+    const size_t ssmem = static_cast<size_t>(pow2) * 4;
+    cudaFuncSetAttribute(sgqa::attn_plan_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssmem);
+    sgqa::attn_plan_sort_kernel<<<static_cast<unsigned>(units), sgqa::kPlanSortThreads, ssmem, st>>>(
+        sel, sel_count, nq, G, k, pow2, q0, B, ids, msk, cnt);
+    SGQA_LAUNCH_CHECK("attn_plan_sort_kernel");
+  }
+  return SGQA_OK;
+}
+
 template <int B>
 sgqa_status launch_attn(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, const void* q, const KvSource& kv,
                         const int32_t* sel, const int32_t* sel_count, void* out, const void* gate, void* ws,
@@ -580,31 +610,11 @@ sgqa_status launch_attn(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq,
     return SGQA_OK;
   }
   const int64_t units = S * ((nq + 7) / 8) * G;
-  const int64_t nbits = std::max<int64_t>((q0 + nq - 1) / B, 1);
-  const int nwords = static_cast<int>((nbits + 31) / 32);
   int32_t* ids = ws_at<int32_t>(ws, w.ids_off);
   uint8_t* msk = ws_at<uint8_t>(ws, w.mask_off);
   int32_t* cnt = ws_at<int32_t>(ws, w.cnt_off);
-  // bitmap, prefix of every word (or, for wide id ranges, of every eighth), masks
-  auto plan_smem = [&](int pshift) {
-    return static_cast<size_t>(nwords) * 4 + static_cast<size_t>(((nwords - 1) >> pshift) + 2) * 4 +
-           static_cast<size_t>(k) * 8;
-  };
-  const int pshift = plan_smem(0) <= 96 * 1024 ? 0 : 3;
-  const size_t psmem = plan_smem(pshift);
-  if (psmem <= 200 * 1024) {
-    cudaFuncSetAttribute(sgqa::attn_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
-    sgqa::attn_plan_kernel<<<static_cast<unsigned>(units), sgqa::kPlanThreads, psmem, st>>>(
-        sel, sel_count, nq, G, k, nwords, pshift, q0, B, ids, msk, cnt);
-    SGQA_LAUNCH_CHECK("attn_plan_kernel");
-  } else {
-    const int pow2 = plan_pow2(k);
-    const size_t ssmem = static_cast<size_t>(pow2) * 4;
-    cudaFuncSetAttribute(sgqa::attn_plan_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssmem);
-    sgqa::attn_plan_sort_kernel<<<static_cast<unsigned>(units), sgqa::kPlanSortThreads, ssmem, st>>>(
-        sel, sel_count, nq, G, k, pow2, q0, B, ids, msk, cnt);
-    SGQA_LAUNCH_CHECK("attn_plan_sort_kernel");
-  }
+  sgqa_status s = launch_plan(p, S, q0, nq, sel, sel_count, ids, msk, cnt, st);
+  if (s != SGQA_OK) return s;
   return launch_attn_tc<B>(p, S, q0, nq, q, kv, ids, msk, cnt, out, gate, units, st);
 }
 
@@ -666,7 +676,9 @@ int q8_splits(const sgqa_params* p, int64_t rows, int64_t max_ctx) {
 }
 
 struct Q8Ws {
-  size_t sums_off, refs_off, bytes;
+  size_t sums_off, refs_off;  // few queries, with weights
+  AttnWs plan;                // many queries: the union plan, and with weights every row's log-sum
+  size_t lse_off, bytes;
 };
 Q8Ws attn_q8_ws(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
   Q8Ws w{};
@@ -679,6 +691,9 @@ Q8Ws attn_q8_ws(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
     w.bytes = w.refs_off + align256(rows * tiles * sgqa::kHg * 4);
     return w;
   }
+  w.plan = attn_ws(p, S, nq);
+  w.lse_off = w.plan.bytes;
+  w.bytes = w.lse_off + (weights ? align256(rows * sgqa::kHg * 4) : 0);
   return w;
 }
 size_t attn_q8_ws_bytes(const sgqa_params* p, int64_t S, int64_t nq, bool weights) {
@@ -749,12 +764,28 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
     SGQA_LAUNCH_CHECK("attn_q8_decode_kernel");
     return SGQA_OK;
   }
-  const size_t smem = sizeof(sgqa::Q8SimpleSmem);
-  cudaFuncSetAttribute(sgqa::attn_q8_simple_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  sgqa::attn_q8_simple_kernel<<<static_cast<unsigned>(rows), sgqa::kQ8SimpleThreads, smem, st>>>(
-      static_cast<const __nv_bfloat16*>(q), c.kv8, c.scale, sel, sel_count, static_cast<const __nv_bfloat16*>(gate),
-      static_cast<__nv_bfloat16*>(out), acc, nq, p->num_kv_groups, p->topk, q0, c.blocks, scale_log2);
-  SGQA_LAUNCH_CHECK("attn_q8_simple_kernel");
+  const int64_t units = S * ((nq + 7) / 8) * p->num_kv_groups;
+  int32_t* ids = ws_at<int32_t>(ws, w.plan.ids_off);
+  uint8_t* msk = ws_at<uint8_t>(ws, w.plan.mask_off);
+  int32_t* cnt = ws_at<int32_t>(ws, w.plan.cnt_off);
+  sgqa_status s = launch_plan(p, S, q0, nq, sel, sel_count, ids, msk, cnt, st);
+  if (s != SGQA_OK) return s;
+  CUtensorMap m;
+  if ((s = q8_map(c, p->num_kv_groups, S, &m)) != SGQA_OK) return s;
+  float* lse = acc != nullptr ? ws_at<float>(ws, w.lse_off) : nullptr;
+  static_assert(sizeof(sgqa::QpSmem) + 1024 <= 232448, "attention tile exceeds shared memory");
+  const size_t smem = sizeof(sgqa::QpSmem) + 1024;
+  // as launch_attn_tc: short selections of a long context leave pairs of blocks unattended by a whole warp
+  const bool skip_pairs = (q0 + nq - 1) / sgqa::kQ8Tok > 4 * static_cast<int64_t>(p->topk);
+  auto kern = skip_pairs ? sgqa::attn_q8_prefill_kernel<false, true> : sgqa::attn_q8_prefill_kernel<false, false>;
+  for (int sweep = 0; sweep < (acc != nullptr ? 2 : 1); ++sweep) {
+    if (sweep == 1) kern = sgqa::attn_q8_prefill_kernel<true, false>;
+    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kern<<<static_cast<unsigned>(units), sgqa::kQpThreads, smem, st>>>(
+        m, static_cast<const __nv_bfloat16*>(q), c.scale, ids, msk, cnt, static_cast<const __nv_bfloat16*>(gate),
+        static_cast<__nv_bfloat16*>(out), lse, acc, nq, p->num_kv_groups, p->topk, q0, c.blocks, scale_log2);
+    SGQA_LAUNCH_CHECK("attn_q8_prefill_kernel");
+  }
   return SGQA_OK;
 }
 

@@ -66,7 +66,11 @@ def quantise_rows(rows: np.ndarray):
 
 def attention(q, kv8, scale, sel, cnt, q_pos0, gate=None):
     """q [S, nq, G*16, D], kv8 [S, blocks, G, 2, 8, D] values, scale [S, blocks, G, 2], sel [S, nq, G, k] (numpy, float64):
-    out, spread (sum of weight * |v|, times the gate) and weights [S, blocks]."""
+    out, the tolerance of out (below) and weights [S, blocks].
+
+    Tolerance: 2^-8 |out| for the result's rounding to BF16, 2^-8 sum w |v| for the weights, 2^-10 sum w |v| for scores,
+    exponentials and sums, and what is below the smallest weight a row resolves: a weight w enters the product as w vs
+    (vs: its V scale) in at least 2^-33 of the row's largest w vs, so it is off by up to half of that times its code."""
     S, nq = q.shape[:2]
     G = kv8.shape[2]
     out, spread = np.zeros(q.shape), np.zeros(q.shape)
@@ -84,14 +88,24 @@ def attention(q, kv8, scale, sel, cnt, q_pos0, gate=None):
                 w = np.exp(s - s.max(1, keepdims=True))
                 w /= w.sum(1, keepdims=True)
                 out[b, i, g * HG:(g + 1) * HG] = w @ V
-                spread[b, i, g * HG:(g + 1) * HG] = w @ np.abs(V)
+                vs = np.repeat(scale[b, ids, g, 1], B)[:n]
+                floor = 2.0 ** -34 * (w * vs).max(1)[:, None] * np.abs(V / vs[:, None]).sum(0)
+                spread[b, i, g * HG:(g + 1) * HG] = (2.0 ** -8 + 2.0 ** -10) * (w @ np.abs(V)) + floor
                 per = np.zeros(len(ids) * B)
                 per[:n] = w.sum(0)
                 np.add.at(weights[b], ids, per.reshape(-1, B).sum(1))
     if gate is not None:
         f = 1.0 / (1.0 + np.exp(-gate))[..., None]
         out, spread = out * f, spread * f
-    return out, spread, weights
+    return out, 2.0 ** -8 * np.abs(out) + spread + 1e-30, weights
+
+
+def check_out(got, ref, tol):
+    got = got.cpu().double().numpy()
+    assert np.isfinite(got).all()
+    off = np.abs(got - ref) / tol
+    at = np.unravel_index(off.argmax(), off.shape)
+    assert off.max() <= 1, (off.max(), at, got[at], ref[at], int((off > 1).sum()))
 
 
 def evict(n, part, keep, first, recent, acc, pos, known, evicted):

@@ -611,15 +611,17 @@ struct __align__(1024) QpSmem {
   uint8_t v16[2][kQpTile][3][1024];          // widened V: [block][chunk][8 rows x 128 B], 128-byte swizzle
   uint8_t k[kQpStages][kQpTile][3][8][64];   // [block][chunk][8 rows][64 B], 64-byte swizzle
   uint8_t v[kQpVStages][kQpTile][3][8][64];
-  float4 meta[kQpMeta][32];                 // per block: K scale, log2(V scale), 1 / V scale, V scale finite (1) or not (0)
+  float4 meta[kQpMeta][32];                 // per block: K scale, log2(V scale), 1 / V scale (NaN scales as 0, 0, 1)
   float4 meta_cur[8];                       // of the current blocks (two are used)
+  uint32_t meta_nan[kQpMeta + 1];           // batch (last: the current blocks): bit i: block i's K or V scale is NaN
+  uint32_t meta_nan_k[kQpMeta + 1];         // its K scale is
   int32_t ids[kQpMeta][32];                 // WEIGHTS: the blocks
   uint64_t q_full;
   uint64_t k_full[kQpStages], k_empty[kQpStages], v_full[kQpVStages], v_empty[kQpVStages], meta_full[kQpMeta];
   uint64_t w_full[2], w_empty[2];           // widened V
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t o_final, drain, drain_pv;
-  float pmax[2][2][128];                    // per tile parity and warp of a pair: the rows' largest score
+  float pmax[2][128];                       // a new reference: the rows' largest scores of the two warps of a pair
   float lsum[2][128];                       // partial row sums of the two warps of a pair
   float gfac[128];
   uint32_t tmem;
@@ -704,18 +706,27 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         const int idx = 32 * bt + lane;
         return idx < U ? uid[idx] : -1;
       };
-      auto scales = [&](int64_t blk) -> float4 {
-        if (blk < 0) return make_float4(0.f, 0.f, 1.f, 1.f);
-        const float2 s = __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g);
-        const bool fin = s.y == s.y;
-        return make_float4(s.x, fin ? log2f(s.y) : 0.f, fin ? 1.f / s.y : 1.f, fin ? 1.f : 0.f);
+      auto scales = [&](int64_t blk) -> float2 {
+        return blk < 0 ? make_float2(0.f, 1.f)
+                       : __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g);
+      };
+      auto publish = [&](float4* dst, int slot, float2 x) {  // by the whole warp
+        const bool nk = !(x.x == x.x), nv = !(x.y == x.y);
+        if (dst != nullptr) *dst = make_float4(nk ? 0.f : x.x, nv ? 0.f : log2f(x.y), nv ? 1.f : 1.f / x.y, 0.f);
+        const uint32_t bk = __ballot_sync(0xffffffffu, nk), bv = __ballot_sync(0xffffffffu, nv);
+        if (lane == 0) {
+          sm.meta_nan[slot] = bk | bv;
+          sm.meta_nan_k[slot] = bk;
+        }
+        __syncwarp();
       };
       if (!WEIGHTS || is_k) {
         int32_t ids_cur = load_batch(0), ids_next = n_union_tiles > 4 ? load_batch(1) : -1;
-        float4 sc_next = make_float4(0.f, 0.f, 1.f, 1.f);
+        float2 sc_next = make_float2(0.f, 1.f);
         if (is_k) {
-          if (lane < 8) sm.meta_cur[lane] = scales(lane == 0 || (lane == 1 && c0 + 8 <= t_last) ? cb + lane : -1);
-          sm.meta[0][lane] = scales(ids_cur);
+          publish(lane < 8 ? &sm.meta_cur[lane] : nullptr, kQpMeta,
+                  scales(lane == 0 || (lane == 1 && c0 + 8 <= t_last) ? cb + lane : -1));
+          publish(&sm.meta[0][lane], 0, scales(ids_cur));
           sm.ids[0][lane] = ids_cur;
           tc::mbar_arrive(bar(sm.meta_full[0]));
           sc_next = scales(ids_next);
@@ -730,7 +741,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
               // Batch bt - 4 was read: this stage's last QK (tile j - 8) waited for the
               // score buffer of tile j - 10, which the softmax frees after its scales.
               if (j >= kQpStages && !tc::warp_wait(bar(sm.k_empty[s]), ((j / kQpStages) - 1) & 1, abort)) break;
-              sm.meta[bt % kQpMeta][lane] = sc_next;
+              publish(&sm.meta[bt % kQpMeta][lane], bt % kQpMeta, sc_next);
               sm.ids[bt % kQpMeta][lane] = ids_cur;
               tc::mbar_arrive(bar(sm.meta_full[bt % kQpMeta]));
             }
@@ -911,7 +922,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // lsum is reused at the end
     }
     float ref = -INFINITY, l = 0.f;  // the row's reference; this warp's part of the sum, relative to 2^ref
-    bool nan_v = false;              // the row attends a block whose V holds an infinity or NaN
+    uint32_t nan_v = 0, nan_k = 0;   // the row attends a block whose V (or K), its K, holds an infinity or NaN
     const float row_lse = WEIGHTS ? (qvalid ? lse[orow_idx] : INFINITY) : 0.f;
     bool ok = tc::mbar_wait(bar(sm.meta_full[0]), 0, abort);  // (the current blocks' scales come with it)
     uint32_t mb_next = 0;  // mask bytes of this warp's blocks of the next tile
@@ -919,34 +930,30 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     for (int j = 0; j < n_tiles; ++j) {
       const int b = j % 2;
       const bool last = j >= n_union_tiles;  // the current-block tile
+      const int slot = last ? kQpMeta : (j / 4) % kQpMeta, at = last ? 4 * half : 8 * (j & 3) + 4 * half;
       const uint32_t tS = tS0 + kSBuf * b + 32 * half + lane_off;
-      const uint32_t mb = mb_next;
+      // bit 8 e: the row's query attends this warp's block e (the plan's bytes
+      // behind the union are zeros)
+      uint32_t use = last ? (half == 0 ? 1u << (8 * (t / 8 - cb)) : 0u) : (mb_next >> qs) & 0x01010101u;
       if (j + 1 < n_union_tiles) mb_next = *reinterpret_cast<const uint32_t*>(umask + 8 * (j + 1) + 4 * half);
-      // bit e: the row's query attends this warp's block e
-      uint32_t bmask;
-      const float4* meta;
-      if (!last) {
-        bmask = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * j + 4 * half + e < U) bmask |= ((mb >> (8 * e + qs)) & 1u) << e;
-        ok = ok && tc::mbar_wait(bar(sm.meta_full[(j / 4) % kQpMeta]), (j / (4 * kQpMeta)) & 1, abort);
-        meta = &sm.meta[(j / 4) % kQpMeta][8 * (j & 3) + 4 * half];
-      } else {
-        bmask = half == 0 ? 1u << (t / 8 - cb) : 0u;
-        meta = &sm.meta_cur[4 * half];
-      }
-      // per block: the score factor, log2 and inverse of the V scale; a block the
-      // row does not attend has factor 0 and offset -inf
+      if (!last && (j & 3) == 0) ok = ok && tc::mbar_wait(bar(sm.meta_full[slot]), (j / (4 * kQpMeta)) & 1, abort);
+      const float4* meta = last ? &sm.meta_cur[at] : &sm.meta[slot][at];
+      // per block: the score factor, log2 and inverse of the V scale
       float cf[4], lv[4], iv[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 mt = meta[e];
-        const bool use = (bmask >> e) & 1u;
-        cf[e] = use ? mt.x * rc : 0.f;
-        lv[e] = use ? mt.y : -INFINITY;
-        iv[e] = use ? mt.z : 0.f;
-        nan_v = nan_v || (use && mt.w == 0.f);
+        cf[e] = mt.x * rc;
+        lv[e] = (use >> (8 * e)) & 1u ? mt.y : -INFINITY;
+        iv[e] = mt.z;
+      }
+      if (const uint32_t nan = sm.meta_nan[slot] >> at) {  // rare
+        const uint32_t nk = sm.meta_nan_k[slot] >> at;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          nan_v |= (use >> (8 * e)) & (nan >> e) & 1u;
+          nan_k |= (use >> (8 * e)) & (nk >> e) & 1u;
+        }
       }
       int32_t tile_id = 0;
       if (WEIGHTS)
@@ -971,7 +978,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         const int end = static_cast<int>(t - c0);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (x > end && ((bmask >> (x >> 3)) & 1u)) sr[x] = __float_as_uint(-INFINITY);
+          if (x > end && ((use >> (8 * (x >> 3))) & 1u)) sr[x] = __float_as_uint(-INFINITY);
       }
       if constexpr (WEIGHTS) {
         // weights of the row, summed by block, then over the warp's 32 rows: lane
@@ -983,7 +990,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
 #pragma unroll
           for (int x = 0; x < 8; ++x) p[x] = fast_exp2(fmaf(__uint_as_float(sr[8 * e + x]), cf[e], -row_lse));
           w[e] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-          if (!((bmask >> e) & 1u) || !(w[e] == w[e]) || !qvalid) w[e] = 0.f;
+          if (!((use >> (8 * e)) & 1u) || !(w[e] == w[e])) w[e] = 0.f;
         }
         float z[2];
         const bool h2 = lane & 2, h1 = lane & 1;
@@ -994,60 +1001,83 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane < 4 && v > 0.f) acc_add(acc + seq * blocks + tile_id, v);
       } else {
-        float bm[4];
+        // Weights with the reference as it is; only where one is above 2^15 (or the
+        // row has no reference yet) is the row's largest score looked for.
+        uint32_t pk[16];
+        float ls;
+        const uint32_t wuse = SKIP_PAIRS ? __reduce_or_sync(0xffffffffu, use) : 0x01010101u;
+        for (int pass = 0; pass < 2; ++pass) {
+          const float neg = ref == -INFINITY ? 0.f : -ref;
+          ls = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float* x = reinterpret_cast<const float*>(&sr[8 * e]);
-          const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          bm[e] = fmaf(mx, cf[e], lv[e]);
-        }
-        sm.pmax[b][half][m] = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3]));
-        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-        const float mraw = fmaxf(sm.pmax[b][0][m], sm.pmax[b][1][m]);
-        // a new reference lies 8 below the largest weight and stays until one exceeds
-        // 2^15: FP16 then holds weights down to 2^-22 of the largest in full
-        const bool need = mraw > ref + 15.f;  // (ref -inf: the first attended block)
-        if (__any_sync(0xffffffffu, need)) {
-          const float old = ref;
-          if (need) ref = mraw - 8.f;
-          const float alpha = need ? exp2f(old - ref) : 1.f;
-          l *= alpha;  // (0, or NaN, while the reference is -inf)
-          if (j > 0) {
-            // O must hold P(j-1) V(j-1) before it is rescaled; each warp of the pair takes half of its columns
-            ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);
-            tc::fence_after();
-#pragma unroll 1
-            for (int h = 3 * half; h < 3 * half + 3; ++h) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + lane_off + 32 * h, o);
-              tc::tmem_ld_wait();
+          for (int e2 = 0; e2 < 4; e2 += 2) {
+            if (!SKIP_PAIRS || ((wuse >> (8 * e2)) & 0x0101u)) {
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-              tc::tmem_st32(tO + lane_off + 32 * h, o);
+              for (int e = e2; e < e2 + 2; ++e) {
+                // P = 2^(s + log2 vs - ref); a block the row does not attend has offset -inf
+                const uint64_t c2 = pack_f32x2(cf[e], cf[e]), o2 = pack_f32x2(lv[e] + neg, lv[e] + neg);
+                uint64_t pe[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const uint64_t v = fma_f32x2(pack_f32x2(__uint_as_float(sr[8 * e + 2 * x]), __uint_as_float(sr[8 * e + 2 * x + 1])), c2, o2);
+                  const float p0 = fast_exp2(f32x2_lo(v)), p1 = fast_exp2(f32x2_hi(v));
+                  pe[x] = pack_f32x2(p0, p1);
+                  pk[4 * e + x] = pack_f16x2(p0, p1);
+                }
+                const uint64_t sum = add_f32x2(add_f32x2(pe[0], pe[1]), add_f32x2(pe[2], pe[3]));
+                ls = fmaf(f32x2_lo(sum) + f32x2_hi(sum), iv[e], ls);
+              }
+            } else {
+#pragma unroll
+              for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
             }
           }
-        }
-        // P = 2^(s + log2 vs - ref)
-        const float neg = ref == -INFINITY ? 0.f : -ref;
-        uint32_t pk[16];
-        float ls = 0.f;
-        const uint32_t wmask = SKIP_PAIRS ? __reduce_or_sync(0xffffffffu, bmask) : 0xFu;
+          if (pass == 1) break;
+          __half2 top = *reinterpret_cast<__half2*>(&pk[0]);
 #pragma unroll
-        for (int e2 = 0; e2 < 4; e2 += 2) {
-          if (!SKIP_PAIRS || ((wmask >> e2) & 3u)) {
+          for (int x = 1; x < 16; ++x) top = __hmax2(top, *reinterpret_cast<__half2*>(&pk[x]));
+          const bool redo = __half2float(__hmax(__low2half(top), __high2half(top))) > 40000.f || (ref == -INFINITY && use != 0u);
+          int any;
+          asm volatile(
+              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q;\n}"
+              : "=r"(any)
+              : "r"(static_cast<int>(redo)), "r"(pair_bar)
+              : "memory");
+          if (!any) break;
+          float mx = -INFINITY;
 #pragma unroll
-            for (int e = e2; e < e2 + 2; ++e) {
-              const float off = lv[e] + neg;
-              float pe[8];
+          for (int e = 0; e < 4; ++e) {
+            float v = __uint_as_float(sr[8 * e]);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) pe[x] = fast_exp2(fmaf(__uint_as_float(sr[8 * e + x]), cf[e], off));
-              ls = fmaf(((pe[0] + pe[1]) + (pe[2] + pe[3])) + ((pe[4] + pe[5]) + (pe[6] + pe[7])), iv[e], ls);
+            for (int x = 1; x < 8; ++x) v = fmaxf(v, __uint_as_float(sr[8 * e + x]));
+            mx = fmaxf(mx, fmaf(v, cf[e], lv[e]));
+          }
+          sm.pmax[half][m] = mx;
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+          mx = fmaxf(sm.pmax[0][m], sm.pmax[1][m]);
+          // A new reference lies 4 below the largest weight: FP16 then holds weights
+          // down to 2^-18 of it in full and resolves 2^-28 of it, and the reference
+          // stays until the scores grow by 2^11.
+          const bool need = mx > ref + 15.f;
+          const float old = ref;
+          if (need) ref = mx - 4.f;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? exp2f(old - ref) : 1.f;
+            l *= alpha;  // (0, or NaN, while the reference is -inf)
+            if (j > 0) {
+              // O must hold P(j-1) V(j-1) before it is rescaled; each warp of the pair takes half of its columns
+              ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);
+              tc::fence_after();
+#pragma unroll 1
+              for (int h = 3 * half; h < 3 * half + 3; ++h) {
+                uint32_t o[32];
+                tc::tmem_ld32(tO + lane_off + 32 * h, o);
+                tc::tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 4; ++x) pk[4 * e + x] = pack_f16x2(pe[2 * x], pe[2 * x + 1]);
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                tc::tmem_st32(tO + lane_off + 32 * h, o);
+              }
             }
-          } else {
-#pragma unroll
-            for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
           }
         }
         l += ls;
@@ -1063,7 +1093,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     if (!WEIGHTS) {
       ok = ok && tc::mbar_wait(bar(sm.o_final), 0, abort);
       if (nan_v) sm.gfac[m] = __uint_as_float(0x7FC00000u);
-      sm.lsum[half][m] = l;
+      sm.lsum[half][m] = nan_k ? __uint_as_float(0x7FC00000u) : l;
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       const float ltot = sm.lsum[0][m] + sm.lsum[1][m];
       if (ok) {

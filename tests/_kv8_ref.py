@@ -69,8 +69,9 @@ def attention(q, kv8, scale, sel, cnt, q_pos0, gate=None):
     out, the tolerance of out (below) and weights [S, blocks].
 
     Tolerance: 2^-8 |out| for the result's rounding to BF16, 2^-8 sum w |v| for the weights, 2^-10 sum w |v| for scores,
-    exponentials and sums, and what is below the smallest weight a row resolves: a weight w enters the product as w vs
-    (vs: its V scale) in at least 2^-33 of the row's largest w vs, so it is off by up to half of that times its code."""
+    exponentials and sums, and what is below the smallest weight a row resolves.  A weight w enters the product as w vs
+    (vs: its V scale) in units in which the row's largest is at least 2^4: as FP16, whose smallest step there is 2^-24, or
+    as three E5M2 values, the last in steps of 2^-22; so it is off by up to 2^-27 of the row's largest w vs, times its code."""
     S, nq = q.shape[:2]
     G = kv8.shape[2]
     out, spread = np.zeros(q.shape), np.zeros(q.shape)
@@ -89,7 +90,7 @@ def attention(q, kv8, scale, sel, cnt, q_pos0, gate=None):
                 w /= w.sum(1, keepdims=True)
                 out[b, i, g * HG:(g + 1) * HG] = w @ V
                 vs = np.repeat(scale[b, ids, g, 1], B)[:n]
-                floor = 2.0 ** -34 * (w * vs).max(1)[:, None] * np.abs(V / vs[:, None]).sum(0)
+                floor = 2.0 ** -27 * (w * vs).max(1)[:, None] * np.abs(V / vs[:, None]).sum(0)
                 spread[b, i, g * HG:(g + 1) * HG] = (2.0 ** -8 + 2.0 ** -10) * (w @ np.abs(V)) + floor
                 per = np.zeros(len(ids) * B)
                 per[:n] = w.sum(0)

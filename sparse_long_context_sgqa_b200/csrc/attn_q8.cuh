@@ -606,6 +606,8 @@ constexpr int kQpVStages = 4;     // V ring depth (codes)
 constexpr int kQpThreads = 512;   // producers and issuers, V widening, 2 x softmax: a warpgroup each
 constexpr int kQpTile = 8;        // blocks per tile
 constexpr int kQpMeta = 4;        // batches (of 4 tiles) whose scales are held
+// Registers: 512 x 128 at launch = 256 x 80 (the first two warpgroups) + 256 x 176 (softmax).
+constexpr int kQpRegsFew = 80, kQpRegsMany = 176;
 
 struct __align__(1024) QpSmem {
   uint8_t v16[2][kQpTile][3][1024];          // widened V: [block][chunk][8 rows x 128 B], 128-byte swizzle
@@ -621,7 +623,7 @@ struct __align__(1024) QpSmem {
   uint64_t w_full[2], w_empty[2];           // widened V
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t o_final, drain, drain_pv;
-  float pmax[2][128];                       // a new reference: the rows' largest scores of the two warps of a pair
+  float mchain[128];                        // the rows' reference after the latest tile
   float lsum[2][128];                       // partial row sums of the two warps of a pair
   float gfac[128];
   uint32_t tmem;
@@ -672,8 +674,8 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     for (int b = 0; b < kQpMeta; ++b) tc::mbar_init(bar(sm.meta_full[b]), 32);
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(bar(sm.s_full[b]), 1);
-      tc::mbar_init(bar(sm.s_free[b]), 256);
-      tc::mbar_init(bar(sm.p_full[b]), 256);
+      tc::mbar_init(bar(sm.s_free[b]), 128);
+      tc::mbar_init(bar(sm.p_full[b]), 128);
       tc::mbar_init(bar(sm.pv_done[b]), 1);
       tc::mbar_init(bar(sm.w_full[b]), 128);
       tc::mbar_init(bar(sm.w_empty[b]), 1);
@@ -695,6 +697,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
   int issued = 0;
 
   if (warp < 4) {
+    tc::regs_dec<kQpRegsFew>();
     if (warp == 0 || warp == 2) {
       // ---------------------------------------------------------------- producers
       const bool is_k = warp == 0;
@@ -822,6 +825,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     }
   } else if (warp < 8) {
     // ---------------------------------------------------------------- V codes -> FP16
+    tc::regs_dec<kQpRegsFew>();
     // A warp takes six of a tile's 24 (block, chunk) pieces, a lane one 16-byte
     // piece of a row in each: 512 contiguous bytes in, two conflict-free 16-byte
     // stores per lane out.
@@ -862,13 +866,16 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     }
   } else {
     // ---------------------------------------------------------------- softmax + epilogue
-    // Two warps per TMEM lane quadrant share every tile: warp `half` takes blocks
-    // 4 half .. 4 half + 3 of its 32 rows.  (Half the registers and code of a whole
-    // tile per warp: with 64 columns unrolled the instruction cache missed on every
-    // tile.)  The two exchange their maxima through shared memory.  A failed wait
-    // clears `ok` but keeps every barrier step in place.
+    tc::regs_inc<kQpRegsMany>();
+    // Two warps per TMEM lane quadrant take alternate tiles (`half`: which), so that
+    // one's exponentials run beside the other's loads and stores.  A tile's weights
+    // are computed with the row's reference as this warp knows it; before they
+    // count, the other warp's decision on the tile before is picked up (bar.sync;
+    // published by bar.arrive), and where a reference moved, or has to, they are
+    // computed once more.  A failed wait clears `ok` but keeps every barrier step.
     const int quad = warp & 3, half = (warp - 8) >> 2;
     const int pair_bar = 1 + quad;
+    const int pub_mine = 5 + 2 * quad + half, pub_other = 5 + 2 * quad + (half ^ 1);
     const int m = quad * 32 + lane;  // TMEM lane = row = (query slot, head)
     const int qs = m >> 4;
     const int64_t qi = qb * 8 + qs;
@@ -921,170 +928,173 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       tc::mbar_arrive(bar(sm.q_full));
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // lsum is reused at the end
     }
-    float ref = -INFINITY, l = 0.f;  // the row's reference; this warp's part of the sum, relative to 2^ref
+    float ref = -INFINITY;           // the row's reference, as this warp knows it
+    float m_l = -INFINITY, l = 0.f;  // this warp's part of the row's sum, relative to 2^m_l
     uint32_t nan_v = 0, nan_k = 0;   // the row attends a block whose V (or K), its K, holds an infinity or NaN
     const float row_lse = WEIGHTS ? (qvalid ? lse[orow_idx] : INFINITY) : 0.f;
     bool ok = tc::mbar_wait(bar(sm.meta_full[0]), 0, abort);  // (the current blocks' scales come with it)
-    uint32_t mb_next = 0;  // mask bytes of this warp's blocks of the next tile
-    if (n_union_tiles > 0) mb_next = *reinterpret_cast<const uint32_t*>(umask + 4 * half);
-    for (int j = 0; j < n_tiles; ++j) {
-      const int b = j % 2;
+    uint2 mb_next = make_uint2(0u, 0u);  // mask bytes of this warp's next tile
+    if (half < n_union_tiles) mb_next = *reinterpret_cast<const uint2*>(umask + 8 * half);
+    for (int j = half; j < n_tiles; j += 2) {
+      const int b = half;
       const bool last = j >= n_union_tiles;  // the current-block tile
-      const int slot = last ? kQpMeta : (j / 4) % kQpMeta, at = last ? 4 * half : 8 * (j & 3) + 4 * half;
-      const uint32_t tS = tS0 + kSBuf * b + 32 * half + lane_off;
-      // bit 8 e: the row's query attends this warp's block e (the plan's bytes
+      const int slot = last ? kQpMeta : (j / 4) % kQpMeta, at = last ? 0 : 8 * (j & 3);
+      const uint32_t tS = tS0 + kSBuf * b + lane_off, tP = tP0 + 32 * b + lane_off;
+      // bit 8 e of word h: the row's query attends block 4 h + e (the plan's bytes
       // behind the union are zeros)
-      uint32_t use = last ? (half == 0 ? 1u << (8 * (t / 8 - cb)) : 0u) : (mb_next >> qs) & 0x01010101u;
-      if (j + 1 < n_union_tiles) mb_next = *reinterpret_cast<const uint32_t*>(umask + 8 * (j + 1) + 4 * half);
-      if (!last && (j & 3) == 0) ok = ok && tc::mbar_wait(bar(sm.meta_full[slot]), (j / (4 * kQpMeta)) & 1, abort);
-      const float4* meta = last ? &sm.meta_cur[at] : &sm.meta[slot][at];
-      // per block: the score factor, log2 and inverse of the V scale
-      float cf[4], lv[4], iv[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 mt = meta[e];
-        cf[e] = mt.x * rc;
-        lv[e] = (use >> (8 * e)) & 1u ? mt.y : -INFINITY;
-        iv[e] = mt.z;
-      }
-      if (const uint32_t nan = sm.meta_nan[slot] >> at) {  // rare
+      const uint32_t use[2] = {last ? 1u << (8 * (t / 8 - cb)) : (mb_next.x >> qs) & 0x01010101u,
+                               last ? 0u : (mb_next.y >> qs) & 0x01010101u};
+      if (j + 2 < n_union_tiles) mb_next = *reinterpret_cast<const uint2*>(umask + 8 * (j + 2));
+      if (!last) ok = ok && tc::mbar_wait(bar(sm.meta_full[slot]), (j / (4 * kQpMeta)) & 1, abort);
+      const float4* meta = last ? sm.meta_cur : &sm.meta[slot][at];
+      if (const uint32_t nan = (sm.meta_nan[slot] >> at) & 0xFFu) {  // rare
         const uint32_t nk = sm.meta_nan_k[slot] >> at;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          nan_v |= (use >> (8 * e)) & (nan >> e) & 1u;
-          nan_k |= (use >> (8 * e)) & (nk >> e) & 1u;
+        for (int e = 0; e < 8; ++e) {
+          nan_v |= (use[e >> 2] >> (8 * (e & 3))) & (nan >> e) & 1u;
+          nan_k |= (use[e >> 2] >> (8 * (e & 3))) & (nk >> e) & 1u;
         }
       }
-      int32_t tile_id = 0;
-      if (WEIGHTS)
-        tile_id = last ? static_cast<int32_t>(cb) + (lane & 3)
-                       : sm.ids[(j / 4) % kQpMeta][8 * (j & 3) + 4 * half + (lane & 3)];
       ok = ok && tc::mbar_wait(bar(sm.s_full[b]), (j / 2) & 1, abort);
       tc::fence_after();
-      uint32_t sr[32];
-      tc::tmem_ld32(tS, sr);
+      uint32_t sr[64];
+      tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+      tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tc::tmem_ld_wait();
-      if (WEIGHTS) {
-        uint32_t lo[32];
-        tc::tmem_ld32(tS + 64, lo);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 32; ++x)
-          sr[x] = __float_as_uint(fmaf(__uint_as_float(lo[x]), 0.0625f, __uint_as_float(sr[x])));
-      }
-      tc::fence_before();
-      tc::mbar_arrive(bar(sm.s_free[b]));
-      if (last && half == 0) {  // tokens of the row's current block behind t
+      if (last) {  // tokens of the row's current block behind t
         const int end = static_cast<int>(t - c0);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (x > end && ((use >> (8 * (x >> 3))) & 1u)) sr[x] = __float_as_uint(-INFINITY);
+          if (x > end && ((use[0] >> (8 * (x >> 3))) & 1u)) sr[x] = __float_as_uint(-INFINITY);
       }
       if constexpr (WEIGHTS) {
         // weights of the row, summed by block, then over the warp's 32 rows: lane
-        // 4 i + e ends with block e
-        float w[4];
+        // 4 i + e ends with block e of its half
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) p[x] = fast_exp2(fmaf(__uint_as_float(sr[8 * e + x]), cf[e], -row_lse));
-          w[e] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-          if (!((use >> (8 * e)) & 1u) || !(w[e] == w[e])) w[e] = 0.f;
-        }
-        float z[2];
-        const bool h2 = lane & 2, h1 = lane & 1;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) z[c] = (h2 ? w[2 + c] : w[c]) + __shfl_xor_sync(0xffffffffu, h2 ? w[c] : w[2 + c], 2);
-        float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane < 4 && v > 0.f) acc_add(acc + seq * blocks + tile_id, v);
-      } else {
-        // Weights with the reference as it is; only where one is above 2^15 (or the
-        // row has no reference yet) is the row's largest score looked for.
-        uint32_t pk[16];
-        float ls;
-        const uint32_t wuse = SKIP_PAIRS ? __reduce_or_sync(0xffffffffu, use) : 0x01010101u;
-        for (int pass = 0; pass < 2; ++pass) {
-          const float neg = ref == -INFINITY ? 0.f : -ref;
-          ls = 0.f;
-#pragma unroll
-          for (int e2 = 0; e2 < 4; e2 += 2) {
-            if (!SKIP_PAIRS || ((wuse >> (8 * e2)) & 0x0101u)) {
-#pragma unroll
-              for (int e = e2; e < e2 + 2; ++e) {
-                // P = 2^(s + log2 vs - ref); a block the row does not attend has offset -inf
-                const uint64_t c2 = pack_f32x2(cf[e], cf[e]), o2 = pack_f32x2(lv[e] + neg, lv[e] + neg);
-                uint64_t pe[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  const uint64_t v = fma_f32x2(pack_f32x2(__uint_as_float(sr[8 * e + 2 * x]), __uint_as_float(sr[8 * e + 2 * x + 1])), c2, o2);
-                  const float p0 = fast_exp2(f32x2_lo(v)), p1 = fast_exp2(f32x2_hi(v));
-                  pe[x] = pack_f32x2(p0, p1);
-                  pk[4 * e + x] = pack_f16x2(p0, p1);
-                }
-                const uint64_t sum = add_f32x2(add_f32x2(pe[0], pe[1]), add_f32x2(pe[2], pe[3]));
-                ls = fmaf(f32x2_lo(sum) + f32x2_hi(sum), iv[e], ls);
-              }
-            } else {
-#pragma unroll
-              for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
-            }
+        for (int h = 0; h < 2; ++h) {
+          uint32_t lo[32];
+          tc::tmem_ld32(tS + 64 + 32 * h, lo);
+          tc::tmem_ld_wait();
+          if (h == 1) {
+            tc::fence_before();
+            tc::mbar_arrive(bar(sm.s_free[b]));
           }
-          if (pass == 1) break;
-          __half2 top = *reinterpret_cast<__half2*>(&pk[0]);
-#pragma unroll
-          for (int x = 1; x < 16; ++x) top = __hmax2(top, *reinterpret_cast<__half2*>(&pk[x]));
-          const bool redo = __half2float(__hmax(__low2half(top), __high2half(top))) > 40000.f || (ref == -INFINITY && use != 0u);
-          int any;
-          asm volatile(
-              "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.s32 %0, 1, 0, q;\n}"
-              : "=r"(any)
-              : "r"(static_cast<int>(redo)), "r"(pair_bar)
-              : "memory");
-          if (!any) break;
-          float mx = -INFINITY;
+          float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
+            const float cf = meta[4 * h + e].x * rc;
+            float p[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              p[x] = fast_exp2(fmaf(fmaf(__uint_as_float(lo[8 * e + x]), 0.0625f, __uint_as_float(sr[32 * h + 8 * e + x])), cf, -row_lse));
+            w[e] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            if (!((use[h] >> (8 * e)) & 1u) || !(w[e] == w[e])) w[e] = 0.f;
+          }
+          float z[2];
+          const bool h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) z[c] = (h2 ? w[2 + c] : w[c]) + __shfl_xor_sync(0xffffffffu, h2 ? w[c] : w[2 + c], 2);
+          float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane < 4 && v > 0.f)
+            acc_add(acc + seq * blocks + (last ? static_cast<int32_t>(cb) + lane : sm.ids[slot][at + 4 * h + lane]), v);
+        }
+      } else {
+        tc::fence_before();
+        tc::mbar_arrive(bar(sm.s_free[b]));
+        // P buffer b is free once O += P(j-2) V(j-2) has read it
+        if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j / 2) - 1) & 1, abort);
+        tc::fence_after();
+        float ls;
+        for (int pass = 0; pass < 2; ++pass) {
+          const float neg = ref == -INFINITY ? 0.f : -ref;
+          __half2 top = __float2half2_rn(0.f);
+          ls = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+            const uint32_t wuse = SKIP_PAIRS ? __reduce_or_sync(0xffffffffu, use[h]) : 0x01010101u;
+#pragma unroll
+            for (int e2 = 0; e2 < 4; e2 += 2) {
+              if (!SKIP_PAIRS || ((wuse >> (8 * e2)) & 0x0101u)) {
+#pragma unroll
+                for (int e = e2; e < e2 + 2; ++e) {
+                  // P = 2^(s + log2 vs - ref); a block the row does not attend has offset -inf
+                  const float4 mt = meta[4 * h + e];
+                  const float cf = mt.x * rc, off = (use[h] >> (8 * e)) & 1u ? mt.y + neg : -INFINITY;
+                  const uint64_t c2 = pack_f32x2(cf, cf), o2 = pack_f32x2(off, off);
+                  uint64_t pe[4];
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const int at2 = 32 * h + 8 * e + 2 * x;
+                    const uint64_t v = fma_f32x2(pack_f32x2(__uint_as_float(sr[at2]), __uint_as_float(sr[at2 + 1])), c2, o2);
+                    const float p0 = fast_exp2(f32x2_lo(v)), p1 = fast_exp2(f32x2_hi(v));
+                    pe[x] = pack_f32x2(p0, p1);
+                    pk[4 * e + x] = pack_f16x2(p0, p1);
+                  }
+                  const uint64_t sum = add_f32x2(add_f32x2(pe[0], pe[1]), add_f32x2(pe[2], pe[3]));
+                  ls = fmaf(f32x2_lo(sum) + f32x2_hi(sum), mt.z, ls);
+                }
+              } else {
+#pragma unroll
+                for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) top = __hmax2(top, *reinterpret_cast<__half2*>(&pk[x]));
+            tc::tmem_st16(tP + 16 * h, pk);
+          }
+          if (pass == 1) break;
+          // The reference after tile j-1, from the other warp.  These weights stand
+          // unless it moved, a weight is above 2^15, or the row had none yet.
+          float m_prev = -INFINITY;
+          if (j > 0) {
+            asm volatile("bar.sync %0, 64;" ::"r"(pub_other) : "memory");
+            m_prev = sm.mchain[m];
+          }
+          const bool moved = m_prev != ref;
+          const bool high = __half2float(__hmax(__low2half(top), __high2half(top))) > 40000.f || (ref == -INFINITY && (use[0] | use[1]) != 0u);
+          if (!__any_sync(0xffffffffu, moved || high)) break;
+          ref = m_prev;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 mt = meta[e];
             float v = __uint_as_float(sr[8 * e]);
 #pragma unroll
             for (int x = 1; x < 8; ++x) v = fmaxf(v, __uint_as_float(sr[8 * e + x]));
-            mx = fmaxf(mx, fmaf(v, cf[e], lv[e]));
+            mx = fmaxf(mx, (use[e >> 2] >> (8 * (e & 3))) & 1u ? fmaf(v, mt.x * rc, mt.y) : -INFINITY);
           }
-          sm.pmax[half][m] = mx;
-          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-          mx = fmaxf(sm.pmax[0][m], sm.pmax[1][m]);
           // A new reference lies 4 below the largest weight: FP16 then holds weights
           // down to 2^-18 of it in full and resolves 2^-28 of it, and the reference
           // stays until the scores grow by 2^11.
           const bool need = mx > ref + 15.f;
-          const float old = ref;
           if (need) ref = mx - 4.f;
-          if (__any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2f(old - ref) : 1.f;
-            l *= alpha;  // (0, or NaN, while the reference is -inf)
-            if (j > 0) {
-              // O must hold P(j-1) V(j-1) before it is rescaled; each warp of the pair takes half of its columns
-              ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);
-              tc::fence_after();
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+            const float alpha = need ? exp2f(m_prev - ref) : 1.f;
+            // O must hold P(j-1) V(j-1) before it is rescaled.  (This warp knows the
+            // product of tile j-2 done, so tile j-3's too: the phase is tile j-1's.)
+            ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);
+            tc::fence_after();
 #pragma unroll 1
-              for (int h = 3 * half; h < 3 * half + 3; ++h) {
-                uint32_t o[32];
-                tc::tmem_ld32(tO + lane_off + 32 * h, o);
-                tc::tmem_ld_wait();
+            for (int h = 0; h < 6; ++h) {
+              uint32_t o[32];
+              tc::tmem_ld32(tO + lane_off + 32 * h, o);
+              tc::tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                tc::tmem_st32(tO + lane_off + 32 * h, o);
-              }
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tc::tmem_st32(tO + lane_off + 32 * h, o);
             }
           }
         }
+        sm.mchain[m] = ref;
+        if (j + 1 < n_tiles) asm volatile("bar.arrive %0, 64;" ::"r"(pub_mine) : "memory");
+        if (m_l != ref) {
+          l = m_l == -INFINITY ? l : l * exp2f(m_l - ref);  // (at -inf: 0, or NaN)
+          m_l = ref;
+        }
         l += ls;
-        // P buffer b is free once O += P(j-2) V(j-2) has read it
-        if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j / 2) - 1) & 1, abort);
-        tc::fence_after();
-        tc::tmem_st16(tP0 + 32 * b + 16 * half + lane_off, pk);
         tc::tmem_st_wait();
         tc::fence_before();
         tc::mbar_arrive(bar(sm.p_full[b]));
@@ -1093,7 +1103,10 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     if (!WEIGHTS) {
       ok = ok && tc::mbar_wait(bar(sm.o_final), 0, abort);
       if (nan_v) sm.gfac[m] = __uint_as_float(0x7FC00000u);
-      sm.lsum[half][m] = nan_k ? __uint_as_float(0x7FC00000u) : l;
+      // both loops are done: the final reference is in mchain; combine the two partial sums
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      ref = sm.mchain[m];
+      sm.lsum[half][m] = nan_k ? __uint_as_float(0x7FC00000u) : m_l == -INFINITY ? l : l * exp2f(m_l - ref);
       asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
       const float ltot = sm.lsum[0][m] + sm.lsum[1][m];
       if (ok) {

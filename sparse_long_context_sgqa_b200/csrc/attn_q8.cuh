@@ -1,13 +1,16 @@
 // Sparse attention over the 8-bit K/V cache (layout: kv8.cuh) on the tcgen05
 // tensor cores, which take the E4M3 codes as they lie: nothing is widened.
 //
-// A query and a softmax weight are not rounded to 8 bits.  Each is split into
-// two E4M3 values, x = hi + lo / 16 with hi = E4M3(x), lo = E4M3(16 (x - hi)):
-// a BF16 query value (8 significant bits) is carried exactly over 2^13 of
-// range below the row's largest, a weight to 2^-8 of itself.  The two halves
-// are MMA columns (or MMA steps) side by side, so K or V is read once for
-// both.  With one scale per (block, group), a block's K scale multiplies its
-// scores and its V scale its weights.
+// A query is not rounded to 8 bits: it is split into two E4M3 values, x = hi +
+// lo / 16 with hi = E4M3(x), lo = E4M3(16 (x - hi)), which carry a BF16 value (8
+// significant bits) exactly over 2^13 of range below the row's largest.  Softmax
+// weights need more range than E4M3 has: where one token takes most of a row (a
+// sink), the result lies in weights 2^-14 of the largest and below.  Few queries
+// split them into three E5M2 values (2^-9 of a weight, over 2^18 of range), many
+// queries take FP16 weights and V widened to FP16.  The parts of a value are MMA
+// columns (or MMA steps) side by side, so K or V is read once for all.  With one
+// scale per (block, group), a block's K scale multiplies its scores and its V
+// scale its weights.
 //
 // Softmax reference.  The weights that enter the MMA are 2^(s - ref) vs: the
 // reference follows the scores plus the exponent of the V scale, so that blocks
@@ -42,6 +45,20 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t v) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
   return __half22float2(__half2(h));
 }
+// Two weights as three E5M2 values each, x = c0 + c1 / 8 + c2 / 64: every value
+// takes three significant bits, the next one what is left.  In FP16 (11 bits,
+// exact differences; an E5M2 code is the upper byte of an FP16 number).
+__device__ __forceinline__ void split_e5m2(float a, float b, uint32_t (&c)[3]) {
+  __half2 r = __floats2half2_rn(a, b);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    c[i] = static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E5M2));
+    if (i < 2) {
+      const uint32_t v = __byte_perm(c[i], 0u, 0x1404);  // bytes 0, 1 into the upper halves' high bytes
+      r = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&v)), __float2half2_rn(8.f));
+    }
+  }
+}
 // hi and 16 x lo codes of two values (low 16 bits each).
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo, float lo_scale) {
   hi = e4m3x2(a, b);
@@ -56,11 +73,12 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
 //   S^T [128 tokens x 32] = K [128 x 192] Q^T     6 MMAs (M128 N32 K32): columns
 //                           16 heads' hi | 16 heads' lo; K as gathered (K-major)
 //   softmax               one thread per token and half of the heads
-//   O^T [192 dims x 32] += V^T [192 x 128] P^T    2 x 4 MMAs (M128 N32 K32): V as
+//   O^T [192 dims x 48] += V^T [192 x 128] P^T    2 x 4 MMAs (M128 N48 K32): V as
 //                           gathered (MN-major), dims 0-127 and 64-191 (the rows
-//                           computed twice are not read); P through shared memory
+//                           computed twice are not read); P through shared memory,
+//                           columns 16 heads' first, second and third E5M2 values
 // A token's scores never cross threads for a maximum: the reference moves only
-// when some weight exceeds 2^8 (one barrier-or per tile tells), and only then
+// when some weight exceeds 2^15 (one barrier-or per tile tells), and only then
 // are a head's maxima reduced over the tile and O rescaled in TMEM.
 // K and V are gathered by a warp each (16 lanes, one 1.5 KB box per block) into
 // rings of their own: a K stage is free again after its MMA, a V stage only
@@ -72,7 +90,7 @@ constexpr int kQdStages = 2;      // of K and of V
 constexpr int kQdMeta = 8;        // tiles whose scales and masks are held
 constexpr int kQdThreads = 384;   // K and V producers, QK and PV issuers, 8 softmax warps
 constexpr int kQdS = 4;           // score buffers: the QK issuer runs ahead, so that K stages are free early
-constexpr int kQdCols = 256;      // TMEM: S 4 x 32, O 2 x 32
+constexpr int kQdCols = 256;      // TMEM: S 4 x 32, O 2 x 64 (48 used)
 constexpr int kQdMaxSplit = 8;    // splits of a row = one (portable) cluster
 constexpr int kQdStage = kQdTile * kQ8Half;  // bytes of a stage
 
@@ -80,13 +98,13 @@ struct __align__(512) QdSmem {
   uint8_t k[kQdStages][kQdTile][3][8][64];    // [block][chunk of 64 dims][8 rows][64 B], 64-byte swizzle
   uint8_t v[kQdStages][kQdTile][3][8][64];
   uint8_t q[3][32][64];                       // [chunk][16 hi, 16 lo][64 B], 64-byte swizzle
-  uint8_t p[2][kQdTile * kQ8Tok][32];         // [token][16 hi, 16 lo], 32-byte swizzle
+  uint8_t p[kQdTile * kQ8Tok][64];            // [token][16 first, 16 second, 16 third values, unused], 64-byte swizzle
   float2 scale[kQdMeta][kQdTile];             // a tile's blocks: K scale, V scale
   int32_t mask[kQdMeta][kQdTile];             // attended tokens (bits 0-7), floor(log2(V scale)) above them
   float wmax[4][kHg];                         // a reference change: maxima of the four lane quadrants
   float qscale[kHg];
   uint64_t k_full[kQdStages], k_empty[kQdStages], v_full[kQdStages], v_empty[kQdStages], meta_full[kQdMeta];
-  uint64_t s_full[kQdS], s_free[kQdS], p_full[2], pv_done[2], q_full, o_final, drain[2];
+  uint64_t s_full[kQdS], s_free[kQdS], p_full, pv_done, q_full, o_final, drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -158,11 +176,9 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       tc::mbar_init(bar(sm.s_full[b]), 1);
       tc::mbar_init(bar(sm.s_free[b]), 256);
     }
-    for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(bar(sm.p_full[b]), 256);
-      tc::mbar_init(bar(sm.pv_done[b]), 1);
-      tc::mbar_init(bar(sm.drain[b]), 1);
-    }
+    for (int b = 0; b < 2; ++b) tc::mbar_init(bar(sm.drain[b]), 1);
+    tc::mbar_init(bar(sm.p_full), 256);
+    tc::mbar_init(bar(sm.pv_done), 1);
     tc::mbar_init(bar(sm.q_full), 256);
     tc::mbar_init(bar(sm.o_final), 1);
     tc::mbar_fence_init();
@@ -267,28 +283,26 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- O^T += V^T P^T
-    const uint32_t id_pv = tc::idesc_e4m3(128, 32, true, true);
-    // V: 64-dim chunks 512 B apart, 8-token groups one block apart; P: 8-token groups 256 B apart
+    const uint32_t id_pv = tc::idesc_e4m3_e5m2(128, 48, true, true);
+    // V: 64-dim chunks 512 B apart, 8-token groups one block apart; P: 8-token groups 512 B apart
     const uint64_t dv0 = tc::sdesc(smem_u32(&sm.v[0][0][0][0][0]), 512, kQ8Half, tc::kSw64);
-    const uint64_t dp0 = tc::sdesc(smem_u32(&sm.p[0][0][0]), 256, 256, tc::kSw32);
+    const uint64_t dp = tc::sdesc(smem_u32(&sm.p[0][0]), 512, 512, tc::kSw64);
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
-      const int s = j % kQdStages, b = j & 1;
-      ok = tc::warp_wait(bar(sm.v_full[s]), (j / kQdStages) & 1, abort) &&
-           tc::warp_wait(bar(sm.p_full[b]), (j >> 1) & 1, abort);
+      const int s = j % kQdStages;
+      ok = tc::warp_wait(bar(sm.v_full[s]), (j / kQdStages) & 1, abort) && tc::warp_wait(bar(sm.p_full), j & 1, abort);
       if (!ok) break;
       tc::fence_after();
       if (tc::elect_one()) {
         const uint64_t dv = dv0 + (kQdStage / 16) * s;
-        const uint64_t dp = dp0 + (kQdTile * kQ8Tok * 32 / 16) * b;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // 32 tokens: V +4 blocks, P +1 KB
+        for (int kk = 0; kk < 4; ++kk) {  // 32 tokens: V +4 blocks, P +2 KB
           const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
-          tc::mma_f8(tO, dv + kk * (4 * kQ8Half / 16), dp + kk * 64, id_pv, acc);
-          tc::mma_f8(tO + 32, dv + 32 + kk * (4 * kQ8Half / 16), dp + kk * 64, id_pv, acc);
+          tc::mma_f8(tO, dv + kk * (4 * kQ8Half / 16), dp + kk * 128, id_pv, acc);
+          tc::mma_f8(tO + 64, dv + 32 + kk * (4 * kQ8Half / 16), dp + kk * 128, id_pv, acc);
         }
         tc::mma_commit(bar(sm.v_empty[s]));
-        tc::mma_commit(bar(sm.pv_done[b]));
+        tc::mma_commit(bar(sm.pv_done));
         if (j + 1 == n_tiles) tc::mma_commit(bar(sm.o_final));
       }
       __syncwarp();
@@ -335,7 +349,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     for (int h = 0; h < 8; ++h) rc[h] = sm.qscale[h0 + h];
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
-      const int b = j & 1, sb = j % kQdS;
+      const int sb = j % kQdS;
       ok = ok && tc::mbar_wait(bar(sm.meta_full[j % kQdMeta]), (j / kQdMeta) & 1, abort);
       const float2 sc = sm.scale[j % kQdMeta][tok >> 3];
       const int32_t msk = sm.mask[j % kQdMeta][tok >> 3];
@@ -355,9 +369,9 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       for (int h = 0; h < 8; ++h) {
         const float v = fmaf(__uint_as_float(sl[h]), 0.0625f, __uint_as_float(sh[h])) * (sc.x * rc[h]);
         x[h] = use ? v : -INFINITY;
-        grow = grow || x[h] + lvs > ref[h] + 8.f;
+        grow = grow || x[h] + lvs > ref[h] + 15.f;
       }
-      // does any weight of the tile exceed 2^8?
+      // does any weight of the tile exceed 2^15?
       int any;
       asm volatile(
           "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
@@ -366,7 +380,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           : "memory");
       if (any) {
         // new references: the largest score (plus log2 of its V scale) - 4, so that
-        // the largest weights stay between 2^4 and 2^8
+        // they stay until the scores grow by 2^11
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const int v = __float_as_int(fmaxf(x[h] + lvs, -INFINITY));
@@ -378,18 +392,18 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const float mx = fmaxf(fmaxf(sm.wmax[0][h0 + h], sm.wmax[1][h0 + h]), fmaxf(sm.wmax[2][h0 + h], sm.wmax[3][h0 + h]));
-          const float nr = mx > ref[h] + 8.f ? mx - 4.f : ref[h];
+          const float nr = mx > ref[h] + 15.f ? mx - 4.f : ref[h];
           al[h] = nr == ref[h] ? 1.f : exp2f(ref[h] - nr);
           ref[h] = nr;
           l[h] *= al[h];
         }
         if (j > 0) {  // O holds P(j-1) V(j-1) by then
-          ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) >> 1) & 1, abort);
+          ok = ok && tc::mbar_wait(bar(sm.pv_done), (j - 1) & 1, abort);
           tc::fence_after();
-#pragma unroll
-          for (int part = 0; part < 4; ++part) {  // dims 0-127, 64-191; hi, lo columns
+#pragma unroll 1
+          for (int part = 0; part < 6; ++part) {  // dims 0-127, 64-191; the three values' columns
             uint32_t o[8];
-            const uint32_t at = tO + 16 * part + h0 + lane_off;
+            const uint32_t at = tO + 64 * (part / 3) + 16 * (part % 3) + h0 + lane_off;
             tc::tmem_ld8(at, o);
             tc::tmem_ld_wait();
 #pragma unroll
@@ -399,7 +413,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           tc::tmem_st_wait();
         }
       }
-      uint32_t hi[2], lo[2];
+      uint32_t p3[3][2];  // the three values of 8 heads
 #pragma unroll
       for (int h = 0; h < 8; h += 2) {
 #pragma unroll
@@ -407,27 +421,19 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           x[h + e] = fast_exp2(x[h + e] - (ref[h + e] == -INFINITY ? 0.f : ref[h + e]));
           l[h + e] += x[h + e];
         }
-        uint32_t a, c;
-        split_e4m3(x[h] * sc.y, x[h + 1] * sc.y, a, c, 16.f);
-        if (h & 2) {
-          hi[h >> 2] |= a << 16;
-          lo[h >> 2] |= c << 16;
-        } else {
-          hi[h >> 2] = a;
-          lo[h >> 2] = c;
-        }
+        uint32_t c[3];
+        split_e5m2(x[h] * sc.y, x[h + 1] * sc.y, c);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) p3[i][h >> 2] = (h & 2) ? p3[i][h >> 2] | (c[i] << 16) : c[i];
       }
-      // P buffer b is free once O += P(j-2) V(j-2) has read it
-      if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j >> 1) - 1) & 1, abort);
-      {
-        uint8_t* pr = &sm.p[b][tok][0] + h0;
-        const uint32_t swz = ((tok >> 2) & 1) << 4;
-        *reinterpret_cast<uint2*>(pr + swz) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(pr + (16 ^ swz)) = make_uint2(lo[0], lo[1]);
-      }
+      // P is free once O += P(j-1) V(j-1) has read it
+      if (j >= 1) ok = ok && tc::mbar_wait(bar(sm.pv_done), (j - 1) & 1, abort);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint2*>(&sm.p[0][0] + sw64_offset(tok, 16 * i + h0)) = make_uint2(p3[i][0], p3[i][1]);
       tc::fence_proxy_async_smem();
       tc::fence_before();
-      tc::mbar_arrive(bar(sm.p_full[b]));
+      tc::mbar_arrive(bar(sm.p_full));
       if (WEIGHTS) {
         // sums over the block's eight tokens (lanes): every exchange halves the
         // heads a lane holds; lane r of a block ends with head r
@@ -477,18 +483,16 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     if (n_tiles > 0) {
       tc::fence_after();
       const int d = quad * 32 + lane;
-      uint32_t hi[8], lo[8];
-      tc::tmem_ld8(tO + h0 + lane_off, hi);
-      tc::tmem_ld8(tO + 16 + h0 + lane_off, lo);
-      tc::tmem_ld_wait();
-#pragma unroll
-      for (int h = 0; h < 8; ++h) po.o[h0 + h][d] = fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h]));
-      if (quad >= 2) {
-        tc::tmem_ld8(tO + 32 + h0 + lane_off, hi);
-        tc::tmem_ld8(tO + 48 + h0 + lane_off, lo);
+      const int parts = quad >= 2 ? 2 : 1;  // dims 0-127; of 64-191 the upper half
+      for (int part = 0; part < parts; ++part) {
+        uint32_t c0[8], c1[8], c2[8];
+        tc::tmem_ld8(tO + 64 * part + h0 + lane_off, c0);
+        tc::tmem_ld8(tO + 64 * part + 16 + h0 + lane_off, c1);
+        tc::tmem_ld8(tO + 64 * part + 32 + h0 + lane_off, c2);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 8; ++h) po.o[h0 + h][64 + d] = fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h]));
+        for (int h = 0; h < 8; ++h)
+          po.o[h0 + h][64 * part + d] = fmaf(fmaf(__uint_as_float(c2[h]), 0.125f, __uint_as_float(c1[h])), 0.125f, __uint_as_float(c0[h]));
       }
     } else {
       for (int x = threadIdx.x - 64; x < kHg * kQdOStride; x += 256) (&po.o[0][0])[x] = 0.f;

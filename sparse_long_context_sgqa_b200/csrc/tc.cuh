@@ -271,9 +271,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major,
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// E4M3 A and E5M2 B (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
 // Shared-memory matrix descriptor with another swizzle: layout type 4 (rows of
-// 64 bytes, 512-byte atoms) or 6 (rows of 32 bytes, 256-byte atoms).
-constexpr uint32_t kSw64 = 4, kSw32 = 6;
+// 64 bytes, 512-byte atoms).
+constexpr uint32_t kSw64 = 4;
 __device__ __forceinline__ uint64_t sdesc(uint32_t smem_addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFF);

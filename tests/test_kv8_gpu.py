@@ -222,6 +222,22 @@ def test_attention_sharp_and_far_scores(Bd, cuda_device, nq):
 
 
 @pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("strength", [12.0, 16.0, 22.0])
+def test_attention_sink(Bd, cuda_device, nq, strength):
+    # one token with V = 0 takes nearly all of every row (e^12 .. e^22 of another token's weight): the result lies in the
+    # small weights of all the others
+    c = make_attn(1, 2, nq, 4001, 500, cuda_device, sigma=0.2)
+    c["sel"][..., 0] = 0
+    c["q"][..., 0] = 4.0
+    c["kv8"][:, 0, :, :, 3] = 0
+    c["kv8"][:, 0, :, 0, 3, 0] = torch.tensor(448.0).to(torch.float8_e4m3fn).view(torch.uint8).to(cuda_device)
+    c["kv8"][:, :, :, 0, :, 0] = torch.where(c["kv8"][:, :, :, 0, :, 0] == c["kv8"][0, 0, 0, 0, 3, 0], c["kv8"][:, :, :, 0, :, 0], 0)
+    c["sc"][:, 0, :, 0] = strength * 192 ** 0.5 / (448 * 4)
+    ref, tol, _ = reference(c)
+    check_attn(c, run_attn(Bd, c), ref, tol)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
 def test_attention_blocks_of_very_different_scale(Bd, cuda_device, nq):
     # V scales over 2^24: the result must be right in every head, also where the weight lies on blocks of small values
     c = make_attn(1, 2, nq, 900, 90, cuda_device, spread=24)

@@ -217,26 +217,33 @@ def alloc_workspace_q8(p: Params, num_seqs: int, nq: int, max_ctx: int, device) 
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
-def _check(name, t, dtype, numel, exact=True):
-    """Address of a contiguous CUDA tensor that holds what the call reads or writes there."""
-    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or (t.numel() != numel if exact else t.numel() < numel):
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {numel} {dtype} values, got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+def _check(name, t, dtype, numel):
+    """Address of a contiguous CUDA tensor of the values the call reads or writes there."""
+    if t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {numel} {dtype} values, got {tuple(t.shape)} "
+                     f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+# the current stream's handle without an object around it, where torch has that (a few microseconds per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(fn, lead, stream, *args):
     """Call fn on the tensors' own device, on the given stream or that device's current one."""
-    dev = lead.device
+    index = lead.get_device()
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-    if dev.index == torch.cuda.current_device():
-        _ok(fn(*args, stream.cuda_stream))
+        raw = _raw_stream(index)
+    elif stream.device.index == index:
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(dev):
-            _ok(fn(*args, stream.cuda_stream))
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {lead.device}")
+    if index == torch.cuda.current_device():
+        _ok(fn(*args, raw))
+    else:
+        with torch.cuda.device(index):
+            _ok(fn(*args, raw))
 
 
 def _q8_cache(p, S, cap, kv8, kv_scale):
@@ -247,7 +254,8 @@ def _q8_cache(p, S, cap, kv8, kv_scale):
 def _workspace(ws):
     if ws is None:
         return None, 0
-    return _check("workspace", ws, torch.uint8, 0, exact=False), ws.numel()
+    n = ws.numel()
+    return _check("workspace", ws, torch.uint8, n), n
 
 
 def sgqa_kv_append_q8(p: Params, num_seqs, cache_cap, pos0, n, k, v, tail, kv8, kv_scale, stream=None):

@@ -8,6 +8,8 @@
 // block found behind it.  At most min(keep, n - keep) blocks move instead of
 // nearly all of them.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 
 namespace sgqa {
@@ -17,8 +19,6 @@ struct EvictArrays {
   uint8_t* base[kMaxArrays];
   int64_t bytes[kMaxArrays];  // per block
   int shift[kMaxArrays];      // log2 of the copied word (1 .. 16 bytes)
-  int tail_only[kMaxArrays];
-  int count;
 };
 
 constexpr int kEvictThreads = 1024;
@@ -65,12 +65,13 @@ __device__ __forceinline__ uint2 evict_scan(uint2 v, uint2* warp_tot, uint2& tot
   return make_uint2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
-// One CTA per sequence: radix select of the smallest kept key (8 bits at a
-// time), then of the largest kept original number among the blocks that tie
-// there; the lists of freed slots and moved blocks; the weights and numbers of
-// the kept blocks in their new slots.
+// Sequences of more blocks than a cluster holds (evict_select_kernel below):
+// one CTA per sequence re-reads the weights for every step.  Radix select of the
+// smallest kept key (8 bits at a time), then of the largest kept original number
+// among the blocks that tie there; the lists of freed slots and moved blocks;
+// the weights and numbers of the kept blocks in their new slots.
 __global__ void __launch_bounds__(kEvictThreads)
-evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64_t evicted, int64_t n, int part,
+evict_select_long_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64_t evicted, int64_t n, int part,
                     int64_t keep, int64_t first, int64_t recent, int64_t slots, EvictWs ws, int64_t* acc_out,
                     int32_t* pos_out) {
   __shared__ uint32_t hist[256];
@@ -191,42 +192,353 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   }
 }
 
-// Moves the blocks' bytes.  A CTA takes the moves of one sequence in turn; a
-// thread copies the same pieces of a block in every step, so that where the
-// incomplete block's new slot held a block that moves, one thread reads each
-// piece before it writes it.
-__global__ void __launch_bounds__(256)
-evict_move_kernel(EvictArrays ar, EvictWs ws, int64_t n, int part, int64_t keep, int64_t slots) {
-  const int64_t seq = blockIdx.y;
-  const int count = ws.count[seq];
-  const int2* moves = ws.moves + seq * ws.cap;
-  auto copy = [&](int64_t to, int64_t from, bool tail) {
-    for (int x = 0; x < ar.count; ++x) {
-      if (ar.tail_only[x] && !tail) continue;
-      uint8_t* dst = ar.base[x] + (seq * slots + to) * ar.bytes[x];
-      const uint8_t* src = ar.base[x] + (seq * slots + from) * ar.bytes[x];
-      const int64_t words = ar.bytes[x] >> ar.shift[x];
-      for (int64_t i = threadIdx.x; i < words; i += blockDim.x) {
-        switch (ar.shift[x]) {
-          case 4: reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i]; break;
-          case 3: reinterpret_cast<uint2*>(dst)[i] = reinterpret_cast<const uint2*>(src)[i]; break;
-          case 2: reinterpret_cast<uint32_t*>(dst)[i] = reinterpret_cast<const uint32_t*>(src)[i]; break;
-          case 1: reinterpret_cast<uint16_t*>(dst)[i] = reinterpret_cast<const uint16_t*>(src)[i]; break;
-          default: dst[i] = src[i];
-        }
-      }
+// ---------------------------------------------------------------------------
+// One cluster per sequence, every CTA a contiguous range of slots whose weights
+// and numbers it keeps in shared memory (12 bytes each, 16384 slots at most).
+// The `keep`-th block of the order (weight down, number up) is found by
+// histograms of 2048 bins that the cluster adds up through distributed shared
+// memory: first on a logarithmic scale (32 bins per power of two, so that
+// weights that fall off over decades spread), then linear in the bin where the
+// boundary lies.  Once at most 512 blocks are left there, they are ranked by
+// counting; usually after two histograms.  Blocks with equal weights that reach
+// the last step are told apart by further histograms of their numbers.
+// Bound: latency (barriers and dependent passes), not bytes.
+// Measured: see evict_move_kernel.
+// ---------------------------------------------------------------------------
+constexpr int kEvBins = 2048;
+constexpr int kEvSlots = 16384;      // per CTA
+constexpr int kEvMaxCluster = 8;     // portable
+constexpr int kEvRank = 512;
+
+struct EvictSmem {
+  uint32_t hist[2][kEvBins];         // two, so that the next pass can clear while others still read
+  uint64_t ckey[kEvRank];            // the last candidates (rank 0's copy is used)
+  uint32_t cpos[kEvRank];
+  uint2 warp_tot[kEvictThreads / 32];
+  uint32_t ccount;
+  uint2 sums;                        // freed slots and moved blocks of this CTA
+  uint32_t bin, above, inside;       // boundary bin, blocks in the bins above it and in it
+  uint64_t tkey;                     // the last kept block
+  uint32_t tpos;
+  int64_t acc[kEvSlots];
+  int32_t pos[kEvSlots];
+};
+
+// Bin of a key on the logarithmic scale: 0 negative weights, 1 none, 2047 protected.
+__device__ __forceinline__ uint32_t evict_log_bin(uint64_t key) {
+  if (key == ~0ull) return kEvBins - 1;
+  if (!(key >> 63)) return 0;
+  const uint64_t a = key ^ 0x8000000000000000ull;
+  if (a == 0) return 1;
+  const int m = 63 - __clzll(static_cast<long long>(a));
+  const uint32_t frac = static_cast<uint32_t>(m >= 5 ? a >> (m - 5) : a << (5 - m)) & 31u;
+  return 2 + 32 * m + frac;
+}
+// Smallest and largest key of a bin.
+__device__ __forceinline__ void evict_log_range(uint32_t bin, uint64_t& lo, uint64_t& hi) {
+  constexpr uint64_t kZero = 0x8000000000000000ull;
+  if (bin == kEvBins - 1) {
+    lo = hi = ~0ull;
+  } else if (bin == 0) {
+    lo = 0;
+    hi = kZero - 1;
+  } else if (bin == 1) {
+    lo = hi = kZero;
+  } else {
+    const int m = static_cast<int>(bin - 2) / 32;
+    const uint64_t f = 32 + (bin - 2) % 32;
+    lo = kZero + (m >= 5 ? f << (m - 5) : f >> (5 - m));
+    hi = m >= 5 ? lo + (1ull << (m - 5)) - 1 : lo;
+  }
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 1)
+evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64_t evicted, int64_t n, int part,
+                    int64_t keep, int64_t first, int64_t recent, int64_t slots, EvictWs ws, int64_t* acc_out,
+                    int32_t* pos_out) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t raw[];
+  EvictSmem& sm = *reinterpret_cast<EvictSmem*>(raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ncta = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int64_t seq = blockIdx.x / ncta;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t recent_from = n + evicted - recent;
+  const int64_t per = (n + ncta - 1) / ncta, s0 = rank * per;
+  const int cnt = static_cast<int>(max(static_cast<int64_t>(0), min(n, s0 + per) - s0));
+  const int64_t* a = acc + seq * slots;
+  const int32_t* p = pos + seq * slots;  // read below `known` only
+  // an odd number of slots per thread: 8-byte reads of neighbours fall in distinct banks
+  const int ipt = static_cast<int>((per + kEvictThreads - 1) / kEvictThreads) | 1;
+  const int i0 = min(tid * ipt, cnt), i1 = min(i0 + ipt, cnt);
+  const int64_t tail_acc = part ? a[n] : 0;
+  for (int i = tid; i < cnt; i += kEvictThreads) {
+    sm.acc[i] = a[s0 + i];
+    sm.pos[i] = evict_pos(p, s0 + i, known, evicted);
+  }
+  for (int i = tid; i < 2 * kEvBins; i += kEvictThreads) (&sm.hist[0][0])[i] = 0;
+  if (tid == 0) sm.ccount = 0;
+  __syncthreads();
+  auto key_at = [&](int i) { return evict_key(sm.acc[i], sm.pos[i], first, recent_from); };
+  // Adds the cluster's histograms and finds, from the highest bin down, the one
+  // with the need-th block; every CTA computes the same.
+  auto boundary = [&](int h, uint32_t need) {
+    cluster.sync();
+    uint32_t c[2] = {0, 0};  // bins 2047 - 2 tid, 2046 - 2 tid
+    for (int r = 0; r < ncta; ++r) {
+      const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[h][kEvBins - 2 - 2 * tid], r));
+      c[0] += v.y;
+      c[1] += v.x;
+    }
+    uint2 tot;
+    const uint32_t before = evict_scan(make_uint2(c[0] + c[1], 0), sm.warp_tot, tot).x;
+    if (before < need && before + c[0] >= need) {
+      sm.bin = kEvBins - 1 - 2 * tid;
+      sm.above = before;
+      sm.inside = c[0];
+    } else if (before + c[0] < need && before + c[0] + c[1] >= need) {
+      sm.bin = kEvBins - 2 - 2 * tid;
+      sm.above = before + c[0];
+      sm.inside = c[1];
+    }
+    __syncthreads();
+    return sm.inside;
+  };
+  auto count = [&](int h, uint32_t bin, bool in) {
+    // warps whose blocks all fall in one bin (no weight, protected) add once
+    const uint32_t live = __ballot_sync(0xffffffffu, in);
+    if (live == 0u) return;
+    const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
+    if (__all_sync(0xffffffffu, !in || bin == lead)) {
+      if (lane == __ffs(live) - 1) atomicAdd(&sm.hist[h][bin], static_cast<uint32_t>(__popc(live)));
+    } else if (in) {
+      atomicAdd(&sm.hist[h][bin], 1u);
     }
   };
-  bool tail_done = false;
-  for (int m = blockIdx.x; m < count; m += gridDim.x) {
-    copy(moves[m].x, moves[m].y, false);
-    if (part && moves[m].y == keep) {
-      copy(keep, n, true);
-      tail_done = true;
+  uint64_t tkey = ~0ull;
+  uint32_t tpos = 0;
+  if (keep > 0) {
+    const int rounds = (cnt + kEvictThreads - 1) / kEvictThreads;
+    uint32_t need = static_cast<uint32_t>(keep);
+    for (int r = 0; r < rounds; ++r) {
+      const int i = r * kEvictThreads + tid;
+      count(0, i < cnt ? evict_log_bin(key_at(i)) : 0u, i < cnt);
+    }
+    uint32_t left = boundary(0, need);
+    need -= sm.above;
+    uint64_t lo, hi;            // the boundary's range of keys, then (by_pos) of numbers, smaller ones first
+    uint32_t plo = 0, phi = 0xFFFFFFFFu;
+    evict_log_range(sm.bin, lo, hi);
+    bool by_pos = lo == hi;
+    int h = 1;
+    while (left > kEvRank && !(by_pos && plo == phi)) {
+      int sh = 0;
+      const uint64_t width = by_pos ? static_cast<uint64_t>(phi - plo) : hi - lo;
+      while ((width >> sh) >= kEvBins) ++sh;
+      for (int r = 0; r < rounds; ++r) {
+        const int i = r * kEvictThreads + tid;
+        bool in = i < cnt;
+        uint32_t bin = 0;
+        if (in) {
+          const uint64_t k = key_at(i);
+          const uint32_t ps = static_cast<uint32_t>(sm.pos[i]);
+          in = k >= lo && k <= hi && (!by_pos || (ps >= plo && ps <= phi));
+          bin = by_pos ? kEvBins - 1 - ((ps - plo) >> sh) : static_cast<uint32_t>((k - lo) >> sh);
+        }
+        count(h, bin, in);
+      }
+      left = boundary(h, need);
+      need -= sm.above;
+      const uint32_t bin = sm.bin;
+      if (by_pos) {
+        plo += (kEvBins - 1 - bin) << sh;
+        phi = static_cast<uint32_t>(min(static_cast<unsigned long long>(phi), plo + ((1ull << sh) - 1)));
+      } else {
+        lo += static_cast<uint64_t>(bin) << sh;
+        hi = min(static_cast<unsigned long long>(hi), lo + ((1ull << sh) - 1));
+        by_pos = lo == hi;
+      }
+      // the histogram before this one has been read by everybody: clear it for the next
+      h ^= 1;
+      for (int i = tid; i < kEvBins; i += kEvictThreads) sm.hist[h][i] = 0;
+      __syncthreads();
+    }
+    if (left > kEvRank) {
+      // more blocks than that with one weight and one number: the call's contract is broken
+      tkey = lo;
+      tpos = phi;
+    } else {
+      // rank the last candidates by counting, in CTA 0
+      EvictSmem* lead = cluster.map_shared_rank(&sm, 0);
+      for (int i = tid; i < cnt; i += kEvictThreads) {
+        const uint64_t k = key_at(i);
+        const uint32_t ps = static_cast<uint32_t>(sm.pos[i]);
+        if (k >= lo && k <= hi && (!by_pos || (ps >= plo && ps <= phi))) {
+          const uint32_t at = atomicAdd(&lead->ccount, 1u);
+          if (at < kEvRank) {
+            lead->ckey[at] = k;
+            lead->cpos[at] = ps;
+          }
+        }
+      }
+      cluster.sync();
+      if (rank == 0) {
+        const uint32_t c = min(sm.ccount, static_cast<uint32_t>(kEvRank));
+        if (tid < static_cast<int>(c)) {
+          const uint64_t k = sm.ckey[tid];
+          const uint32_t ps = sm.cpos[tid];
+          uint32_t better = 0;
+          for (uint32_t i = 0; i < c; ++i) {
+            const uint64_t ki = sm.ckey[i];
+            const uint32_t pi = sm.cpos[i];
+            better += (ki > k || (ki == k && (pi < ps || (pi == ps && i < static_cast<uint32_t>(tid))))) ? 1u : 0u;
+          }
+          if (better == need - 1) {
+            sm.tkey = k;
+            sm.tpos = ps;
+          }
+        }
+      }
+      cluster.sync();
+      tkey = lead->tkey;
+      tpos = lead->tpos;
     }
   }
-  // the first block behind `keep` moves first, if it moves at all: move 0
-  if (blockIdx.x == 0 && part && keep < n && !tail_done) copy(keep, n, true);
+  auto kept = [&](int i) {
+    const uint64_t k = key_at(i);
+    return keep > 0 && (k > tkey || (k == tkey && static_cast<uint32_t>(sm.pos[i]) <= tpos));
+  };
+  // freed slots below `keep`, kept blocks behind it: ranks over the whole sequence
+  uint2 mine = make_uint2(0, 0), tot;
+  uint32_t keeps = 0;  // bit i: kept (ipt <= 17)
+  for (int i = i0; i < i1; ++i) {
+    const bool k = kept(i);
+    keeps |= (k ? 1u : 0u) << (i - i0);
+    if (s0 + i < keep) mine.x += !k;
+    else mine.y += k;
+  }
+  uint2 at = evict_scan(mine, sm.warp_tot, tot);
+  if (tid == 0) sm.sums = tot;
+  cluster.sync();
+  uint2 all = make_uint2(0, 0);
+  for (int r = 0; r < ncta; ++r) {
+    const uint2 v = cluster.map_shared_rank(&sm, r)->sums;
+    if (r < rank) {
+      at.x += v.x;
+      at.y += v.y;
+    }
+    all.x += v.x;
+    all.y += v.y;
+  }
+  int2* moves = ws.moves + seq * ws.cap;
+  int64_t* macc = ws.moved_acc + seq * (ws.cap + 1);
+  int32_t* mpos = ws.moved_pos + seq * ws.cap;
+  uint2 r = at;
+  for (int i = i0; i < i1; ++i) {
+    const bool k = (keeps >> (i - i0)) & 1u;
+    if (s0 + i < keep) {
+      if (!k) moves[r.x++].x = static_cast<int32_t>(s0 + i);
+    } else if (k) {
+      moves[r.y].y = static_cast<int32_t>(s0 + i);
+      macc[r.y] = sm.acc[i];
+      mpos[r.y++] = sm.pos[i];
+    }
+  }
+  if (tid == 0 && rank == 0) {
+    if (all.x != all.y) report(kDevBounds);  // original numbers that occur twice
+    ws.count[seq] = static_cast<int32_t>(min(all.x, all.y));
+  }
+  __threadfence();
+  cluster.sync();  // the lists are complete, and every weight has been read
+  // new weights and numbers: kept blocks that stay, then the moved ones; no weight behind them
+  int64_t* ao = acc_out + seq * slots;
+  int32_t* po = pos_out + seq * slots;
+  uint32_t hole = at.x;
+  for (int i = i0; i < i1; ++i) {
+    const int64_t s = s0 + i;
+    if (s >= keep) break;
+    if ((keeps >> (i - i0)) & 1u) {
+      ao[s] = sm.acc[i];
+      po[s] = sm.pos[i];
+    } else {
+      const bool ok = hole < all.y;
+      ao[s] = ok ? macc[hole] : 0;
+      po[s] = ok ? mpos[hole] : -1;
+      ++hole;
+    }
+  }
+  for (int64_t s = keep + static_cast<int64_t>(rank) * kEvictThreads + tid; s < slots; s += static_cast<int64_t>(ncta) * kEvictThreads)
+    ao[s] = s == keep && part ? tail_acc : 0;
+  cluster.sync();  // no CTA leaves while others may read its shared memory
+}
+
+// ---------------------------------------------------------------------------
+// Moves the blocks' bytes.  The work of a move is cut into pieces of 256 words
+// (4 KB of 16-byte words); a warp copies a piece with eight loads per lane in
+// flight.  Where the incomplete block's new slot held a block that moves (it
+// is the first move then), the warp that takes a piece of that move takes the
+// same piece of the incomplete block after it, with the same lanes.
+// Bound: HBM, every moved byte read and written once.
+// ---------------------------------------------------------------------------
+constexpr int kMovePiece = 256;
+constexpr int kMoveWarps = 8;
+
+template <typename T>
+__device__ __forceinline__ void move_piece(T* dst, const T* src, int64_t w0, int64_t words, int lane) {
+  T v[kMovePiece / 32];
+#pragma unroll
+  for (int i = 0; i < kMovePiece / 32; ++i) {
+    const int64_t w = w0 + 32 * i + lane;
+    if (w < words) v[i] = src[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kMovePiece / 32; ++i) {
+    const int64_t w = w0 + 32 * i + lane;
+    if (w < words) dst[w] = v[i];
+  }
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32)
+evict_move_kernel(EvictArrays ar, EvictWs ws, int64_t n, int part, int64_t keep, int64_t slots, int pieces, int tail_pieces) {
+  const int64_t seq = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int count = ws.count[seq];
+  const int2* moves = ws.moves + seq * ws.cap;
+  // piece q of a move's bytes, arrays in order (those of which only the incomplete block moves last)
+  auto copy = [&](int q, int64_t to, int64_t from) {
+    int x = 0;
+    int64_t per;
+    for (;; ++x) {
+      per = ((ar.bytes[x] >> ar.shift[x]) + kMovePiece - 1) / kMovePiece;
+      if (q < per) break;
+      q -= static_cast<int>(per);
+    }
+    uint8_t* dst = ar.base[x] + (seq * slots + to) * ar.bytes[x];
+    const uint8_t* src = ar.base[x] + (seq * slots + from) * ar.bytes[x];
+    const int64_t words = ar.bytes[x] >> ar.shift[x], w0 = static_cast<int64_t>(q) * kMovePiece;
+    switch (ar.shift[x]) {
+      case 4: move_piece(reinterpret_cast<uint4*>(dst), reinterpret_cast<const uint4*>(src), w0, words, lane); break;
+      case 3: move_piece(reinterpret_cast<uint2*>(dst), reinterpret_cast<const uint2*>(src), w0, words, lane); break;
+      case 2: move_piece(reinterpret_cast<uint32_t*>(dst), reinterpret_cast<const uint32_t*>(src), w0, words, lane); break;
+      case 1: move_piece(reinterpret_cast<uint16_t*>(dst), reinterpret_cast<const uint16_t*>(src), w0, words, lane); break;
+      default: move_piece(dst, src, w0, words, lane);
+    }
+  };
+  const bool tail = part && keep < n;                       // the incomplete block moves to slot `keep`
+  const bool chained = tail && count > 0 && moves[0].y == keep;
+  const int64_t items = static_cast<int64_t>(count) * pieces;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveWarps;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5); it < items + (tail ? tail_pieces : 0); it += step) {
+    if (it < items) {
+      const int64_t m = it / pieces;
+      const int q = static_cast<int>(it - m * pieces);
+      copy(q, moves[m].x, moves[m].y);
+      if (m == 0 && chained) copy(q, keep, n);
+    } else {
+      const int q = static_cast<int>(it - items);
+      if (!chained || q >= pieces) copy(q, keep, n);
+    }
+  }
 }
 
 }  // namespace sgqa

@@ -1214,20 +1214,26 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
   REQUIRE_PTR(acc_out, 8);
   REQUIRE_PTR(pos_out, 4);
   if (pos_count > 0) REQUIRE_PTR(pos, 4);
+  // arrays of which every moved block is copied first, then those of which only the incomplete one is
   sgqa::EvictArrays ar{};
-  ar.count = num_arrays;
-  for (int i = 0; i < num_arrays; ++i) {
+  int64_t pieces = 0, tail_pieces = 0;  // copied per move, and for the incomplete block
+  for (int i = 0; i < num_arrays; ++i)
     if (arrays[i].data == nullptr || arrays[i].block_bytes < 1)
       return fail(SGQA_ERR_INVALID_ARGUMENT, "array %d: NULL or without bytes", i);
-    ar.base[i] = static_cast<uint8_t*>(arrays[i].data);
-    ar.bytes[i] = arrays[i].block_bytes;
-    ar.tail_only[i] = arrays[i].tail_only != 0;
-    int shift = 4;  // the widest word that address and size allow
-    while (shift > 0 && ((reinterpret_cast<uintptr_t>(arrays[i].data) | static_cast<uintptr_t>(arrays[i].block_bytes)) &
-                         ((1u << shift) - 1)))
-      --shift;
-    ar.shift[i] = shift;
-  }
+  for (int pass = 0, x = 0; pass < 2; ++pass)
+    for (int i = 0; i < num_arrays; ++i) {
+      if ((arrays[i].tail_only != 0) != (pass == 1)) continue;
+      int shift = 4;  // the widest word that address and size allow
+      while (shift > 0 && ((reinterpret_cast<uintptr_t>(arrays[i].data) | static_cast<uintptr_t>(arrays[i].block_bytes)) &
+                           ((1u << shift) - 1)))
+        --shift;
+      ar.base[x] = static_cast<uint8_t*>(arrays[i].data);
+      ar.bytes[x] = arrays[i].block_bytes;
+      ar.shift[x++] = shift;
+      const int64_t n_pieces = ((arrays[i].block_bytes >> shift) + sgqa::kMovePiece - 1) / sgqa::kMovePiece;
+      if (pass == 0) pieces += n_pieces;
+      tail_pieces += n_pieces;
+    }
   const EvictLayout l = evict_layout(num_seqs, slots);
   if ((s = check_ws(workspace, workspace_bytes, l.bytes)) != SGQA_OK) return s;
   if (num_seqs > 65535) return fail(SGQA_ERR_UNSUPPORTED, "at most 65535 sequences per call");
@@ -1238,14 +1244,44 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
   ws.moved_pos = ws_at<int32_t>(workspace, l.mpos_off);
   ws.count = ws_at<int32_t>(workspace, l.count_off);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  sgqa::evict_select_kernel<<<static_cast<unsigned>(num_seqs), sgqa::kEvictThreads, 0, st>>>(
-      acc, pos, pos_count, evicted, n, part, keep, first, recent, slots, ws, acc_out, pos_out);
-  SGQA_LAUNCH_CHECK("evict_select_kernel");
-  const int64_t most = std::min(keep, n - keep) + part;  // moves of a sequence
-  if (num_arrays == 0 || keep == n || most == 0) return SGQA_OK;
-  const int64_t per_seq = std::min<int64_t>(most, std::max<int64_t>(1, 8 * kSmCount / num_seqs));
-  sgqa::evict_move_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(num_seqs)), 256, 0, st>>>(
-      ar, ws, n, part, keep, slots);
+  // A cluster per sequence holds up to 131072 blocks (a 1M-token context of
+  // 8-token blocks); about 4096 slots per CTA keep its passes short.
+  const int64_t ncta = std::min<int64_t>(sgqa::kEvMaxCluster, (n + 4095) / 4096);
+  if (n <= static_cast<int64_t>(sgqa::kEvMaxCluster) * sgqa::kEvSlots) {
+    const size_t smem = sizeof(sgqa::EvictSmem);
+    static_assert(sizeof(sgqa::EvictSmem) <= 232448, "select state exceeds shared memory");
+    cudaFuncSetAttribute(sgqa::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaLaunchConfig_t cfg = {};
+    const unsigned cl = static_cast<unsigned>(std::max<int64_t>(ncta, 1));
+    cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * cl);
+    cfg.blockDim = dim3(sgqa::kEvictThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, sgqa::evict_select_kernel, acc, pos, pos_count, evicted, n, part, keep, first,
+                                       recent, slots, ws, acc_out, pos_out);
+    if (e != cudaSuccess) return cuda_fail(e, "evict_select_kernel launch");
+    SGQA_LAUNCH_CHECK("evict_select_kernel");
+  } else {
+    sgqa::evict_select_long_kernel<<<static_cast<unsigned>(num_seqs), sgqa::kEvictThreads, 0, st>>>(
+        acc, pos, pos_count, evicted, n, part, keep, first, recent, slots, ws, acc_out, pos_out);
+    SGQA_LAUNCH_CHECK("evict_select_long_kernel");
+  }
+  const int64_t most = std::min(keep, n - keep);  // moves of a sequence
+  if (num_arrays == 0 || keep == n || (most == 0 && !part)) return SGQA_OK;
+  if (pieces + tail_pieces > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "blocks too large");
+  const int64_t items = most * pieces + (part ? tail_pieces : 0);  // at most
+  const int64_t want = (items + sgqa::kMoveWarps - 1) / sgqa::kMoveWarps;
+  const int64_t per_seq = std::min<int64_t>(want, std::max<int64_t>(1, 8 * kSmCount / num_seqs));
+  sgqa::evict_move_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(num_seqs)),
+                            sgqa::kMoveWarps * 32, 0, st>>>(ar, ws, n, part, keep, slots, static_cast<int>(pieces),
+                                                            static_cast<int>(tail_pieces));
   SGQA_LAUNCH_CHECK("evict_move_kernel");
   return SGQA_OK;
 }

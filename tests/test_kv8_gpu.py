@@ -367,7 +367,9 @@ def evict_case(S, n, part, B_, seed, dev, known, evicted, ties):
     (2, 513, 1, 2, 400, 4, 16, 300, 77, True), (4, 2000, 5, 8, 1999, 1, 1, 0, 0, False), (1, 40, 3, 8, 40, 0, 0, 10, 3, False),
     (2, 3001, 0, 1, 1500, 10, 700, 3001, 11, True), (1, 1200, 4, 8, 600, 300, 300, 500, 5, True),
     (3, 20000, 6, 8, 15000, 4, 64, 15000, 100000, False), (1, 70000, 1, 8, 1000, 0, 0, 0, 0, True),
-    (2, 64, 7, 8, 0, 0, 0, 64, 1, False)])
+    (2, 64, 7, 8, 0, 0, 0, 64, 1, False), (1, 131072, 2, 8, 100000, 4, 512, 0, 0, False), (1, 140000, 0, 1, 30000, 4, 64, 9, 2, False),
+    (2, 16385, 3, 8, 16000, 0, 0, 0, 0, True), (1, 131072, 0, 8, 65536, 0, 0, 131072, 7, True), (1, 4097, 1, 8, 4096, 0, 0, 0, 0, False),
+    (40, 700, 1, 8, 650, 1, 1, 0, 0, False)])
 def test_evict_parity(Bd, cuda_device, S, n, part, B_, keep, first, recent, known, evicted, ties):
     part = part % B_
     slots, acc, pos, arrays, tails = evict_case(S, n, part, B_, n + keep, cuda_device, known, evicted, ties)

@@ -191,6 +191,9 @@ class _Tensor:
     def data_ptr(self):
         return PTR
 
+    def get_device(self):
+        return self.device.index
+
 
 def _append_tensors(**kw):
     t = dict(k=_Tensor((2, 3, 4, 192), torch.bfloat16), v=_Tensor((2, 3, 4, 192), torch.bfloat16),
@@ -212,7 +215,7 @@ def test_tensors_that_do_not_fit_are_refused(kw):
 def test_calls_run_on_the_tensors_device(monkeypatch):
     class Guard:
         def __init__(self, dev):
-            log.append(("enter", str(dev)))
+            log.append(("enter", dev))
 
         def __enter__(self):
             pass
@@ -226,10 +229,10 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     log = []
     monkeypatch.setattr(Bd.torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(Bd.torch.cuda, "device", Guard)
-    monkeypatch.setattr(Bd.torch.cuda, "current_stream", lambda dev: Stream())
+    monkeypatch.setattr(Bd, "_raw_stream", lambda index: 76 + index)
     monkeypatch.setattr(Bd._lib, "sgqa_kv_append_q8", lambda *a: log.append(("call", a[-1])) or 0)
     Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **_append_tensors())
-    assert log == [("enter", "cuda:1"), ("call", 77), "exit"]
+    assert log == [("enter", 1), ("call", 77), "exit"]
     monkeypatch.setattr(Bd.torch.cuda, "current_device", lambda: 1)
     log.clear()
     Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **_append_tensors())

@@ -18,7 +18,7 @@ constexpr int kMaxArrays = 8;
 struct EvictArrays {
   uint8_t* base[kMaxArrays];
   int64_t bytes[kMaxArrays];  // per block
-  int shift[kMaxArrays];      // log2 of the copied word (1 .. 16 bytes)
+  int shift[kMaxArrays];      // log2 of the copied word (16, 4 or 1 bytes)
 };
 
 constexpr int kEvictThreads = 1024;
@@ -272,9 +272,21 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   const int ipt = static_cast<int>((per + kEvictThreads - 1) / kEvictThreads) | 1;
   const int i0 = min(tid * ipt, cnt), i1 = min(i0 + ipt, cnt);
   const int64_t tail_acc = part ? a[n] : 0;
-  for (int i = tid; i < cnt; i += kEvictThreads) {
-    sm.acc[i] = a[s0 + i];
-    sm.pos[i] = evict_pos(p, s0 + i, known, evicted);
+  for (int i = tid; i < cnt; i += 4 * kEvictThreads) {  // four loads of each in flight
+    int64_t va[4];
+    int32_t vp[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x * kEvictThreads < cnt) {
+        va[x] = a[s0 + i + x * kEvictThreads];
+        vp[x] = evict_pos(p, s0 + i + x * kEvictThreads, known, evicted);
+      }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i + x * kEvictThreads < cnt) {
+        sm.acc[i + x * kEvictThreads] = va[x];
+        sm.pos[i + x * kEvictThreads] = vp[x];
+      }
   }
   for (int i = tid; i < 2 * kEvBins; i += kEvictThreads) (&sm.hist[0][0])[i] = 0;
   if (tid == 0) sm.ccount = 0;
@@ -285,11 +297,13 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   auto boundary = [&](int h, uint32_t need) {
     cluster.sync();
     uint32_t c[2] = {0, 0};  // bins 2047 - 2 tid, 2046 - 2 tid
-    for (int r = 0; r < ncta; ++r) {
-      const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[h][kEvBins - 2 - 2 * tid], r));
-      c[0] += v.y;
-      c[1] += v.x;
-    }
+#pragma unroll
+    for (int r = 0; r < kEvMaxCluster; ++r)
+      if (r < ncta) {
+        const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[h][kEvBins - 2 - 2 * tid], r));
+        c[0] += v.y;
+        c[1] += v.x;
+      }
     uint2 tot;
     const uint32_t before = evict_scan(make_uint2(c[0] + c[1], 0), sm.warp_tot, tot).x;
     if (before < need && before + c[0] >= need) {
@@ -388,6 +402,7 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
           const uint64_t k = sm.ckey[tid];
           const uint32_t ps = sm.cpos[tid];
           uint32_t better = 0;
+#pragma unroll 8
           for (uint32_t i = 0; i < c; ++i) {
             const uint64_t ki = sm.ckey[i];
             const uint32_t pi = sm.cpos[i];
@@ -421,15 +436,17 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   if (tid == 0) sm.sums = tot;
   cluster.sync();
   uint2 all = make_uint2(0, 0);
-  for (int r = 0; r < ncta; ++r) {
-    const uint2 v = cluster.map_shared_rank(&sm, r)->sums;
-    if (r < rank) {
-      at.x += v.x;
-      at.y += v.y;
+#pragma unroll
+  for (int r = 0; r < kEvMaxCluster; ++r)
+    if (r < ncta) {
+      const uint2 v = cluster.map_shared_rank(&sm, r)->sums;
+      if (r < rank) {
+        at.x += v.x;
+        at.y += v.y;
+      }
+      all.x += v.x;
+      all.y += v.y;
     }
-    all.x += v.x;
-    all.y += v.y;
-  }
   int2* moves = ws.moves + seq * ws.cap;
   int64_t* macc = ws.moved_acc + seq * (ws.cap + 1);
   int32_t* mpos = ws.moved_pos + seq * ws.cap;
@@ -454,18 +471,19 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   int64_t* ao = acc_out + seq * slots;
   int32_t* po = pos_out + seq * slots;
   uint32_t hole = at.x;
-  for (int i = i0; i < i1; ++i) {
-    const int64_t s = s0 + i;
-    if (s >= keep) break;
-    if ((keeps >> (i - i0)) & 1u) {
-      ao[s] = sm.acc[i];
-      po[s] = sm.pos[i];
-    } else {
+  for (int i = i0; i < i1 && s0 + i < keep; ++i) {
+    if (!((keeps >> (i - i0)) & 1u)) {
       const bool ok = hole < all.y;
-      ao[s] = ok ? macc[hole] : 0;
-      po[s] = ok ? mpos[hole] : -1;
+      sm.acc[i] = ok ? macc[hole] : 0;
+      sm.pos[i] = ok ? mpos[hole] : -1;
       ++hole;
     }
+  }
+  __syncthreads();
+  const int below = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(cnt), keep - s0)));
+  for (int i = tid; i < below; i += kEvictThreads) {
+    ao[s0 + i] = sm.acc[i];
+    po[s0 + i] = sm.pos[i];
   }
   for (int64_t s = keep + static_cast<int64_t>(rank) * kEvictThreads + tid; s < slots; s += static_cast<int64_t>(ncta) * kEvictThreads)
     ao[s] = s == keep && part ? tail_acc : 0;
@@ -473,71 +491,103 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
 }
 
 // ---------------------------------------------------------------------------
-// Moves the blocks' bytes.  The work of a move is cut into pieces of 256 words
-// (4 KB of 16-byte words); a warp copies a piece with eight loads per lane in
-// flight.  Where the incomplete block's new slot held a block that moves (it
-// is the first move then), the warp that takes a piece of that move takes the
-// same piece of the incomplete block after it, with the same lanes.
+// Moves the blocks' bytes, 256 words (4 KB of 16-byte words) per warp and step,
+// eight loads per lane in flight: a piece of one move's block, or, for arrays of
+// at most 128 words per block, as many whole blocks of consecutive moves as fit.
+// Where the incomplete block's new slot held a block that moves (it is the
+// first move then), the lane that copies a word of that move copies the same word
+// of the incomplete block after it.
 // Bound: HBM, every moved byte read and written once.
 // ---------------------------------------------------------------------------
 constexpr int kMovePiece = 256;
 constexpr int kMoveWarps = 8;
 
+// Warp steps that `count` moves of an array with that many words per block take.
+__host__ __device__ inline int64_t move_steps(int64_t words, int64_t count) {
+  if (words > kMovePiece / 2) return count * ((words + kMovePiece - 1) / kMovePiece);
+  const int64_t group = kMovePiece / words;
+  return (count + group - 1) / group;
+}
+
+// One step of large blocks: words [w0, w0 + 256) of a block.
 template <typename T>
-__device__ __forceinline__ void move_piece(T* dst, const T* src, int64_t w0, int64_t words, int lane) {
-  T v[kMovePiece / 32];
+__device__ __forceinline__ void move_large(T* dst, const T* src, int w0, int words, int lane) {
+  src += w0 + lane;
+  dst += w0 + lane;
+  if (w0 + kMovePiece <= words) {
+    T v[kMovePiece / 32];
 #pragma unroll
-  for (int i = 0; i < kMovePiece / 32; ++i) {
-    const int64_t w = w0 + 32 * i + lane;
-    if (w < words) v[i] = src[w];
-  }
+    for (int i = 0; i < kMovePiece / 32; ++i) v[i] = src[32 * i];
 #pragma unroll
-  for (int i = 0; i < kMovePiece / 32; ++i) {
-    const int64_t w = w0 + 32 * i + lane;
-    if (w < words) dst[w] = v[i];
+    for (int i = 0; i < kMovePiece / 32; ++i) dst[32 * i] = v[i];
+  } else {
+#pragma unroll 1
+    for (int w = w0 + lane; w < words; w += 32, src += 32, dst += 32) *dst = *src;
   }
 }
 
-__global__ void __launch_bounds__(kMoveWarps * 32)
-evict_move_kernel(EvictArrays ar, EvictWs ws, int64_t n, int part, int64_t keep, int64_t slots, int pieces, int tail_pieces) {
+// One step of small blocks: the blocks of moves [m0, m0 + 256 / words).
+template <typename T>
+__device__ __forceinline__ void move_small(T* base, int words, int64_t m0, const int2* moves, int64_t count, int lane) {
+  const int group = static_cast<int>(min(static_cast<int64_t>(kMovePiece / words), count - m0));
+#pragma unroll 4
+  for (int x = lane; x < group * words; x += 32) {
+    const int g = x / words, w = x - g * words;
+    const int2 mv = moves[m0 + g];
+    base[static_cast<int64_t>(mv.x) * words + w] = base[static_cast<int64_t>(mv.y) * words + w];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void move_step(T* base, int words, int64_t step, const int2* moves, int64_t count, bool chained,
+                                          int64_t to0, int64_t from0, int lane) {
+  if (words > kMovePiece / 2) {
+    const int per = (words + kMovePiece - 1) / kMovePiece;
+    const int64_t m = step / per;
+    const int w0 = static_cast<int>(step - m * per) * kMovePiece;
+    const int2 mv = moves[m];
+    move_large(base + static_cast<int64_t>(mv.x) * words, base + static_cast<int64_t>(mv.y) * words, w0, words, lane);
+    if (chained && m == 0) move_large(base + to0 * words, base + from0 * words, w0, words, lane);
+  } else {
+    const int64_t m0 = step * (kMovePiece / words);
+    move_small(base, words, m0, moves, count, lane);
+    if (chained && m0 == 0) {  // word w of move 0 was lane w % 32's
+      for (int w = lane; w < words; w += 32) base[to0 * words + w] = base[from0 * words + w];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32, 4)
+evict_move_kernel(const __grid_constant__ EvictArrays ar, int arrays, int tail_arrays, EvictWs ws, int64_t n, int part, int64_t keep, int64_t slots) {
   const int64_t seq = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const int count = ws.count[seq];
   const int2* moves = ws.moves + seq * ws.cap;
-  // piece q of a move's bytes, arrays in order (those of which only the incomplete block moves last)
-  auto copy = [&](int q, int64_t to, int64_t from) {
-    int x = 0;
-    int64_t per;
-    for (;; ++x) {
-      per = ((ar.bytes[x] >> ar.shift[x]) + kMovePiece - 1) / kMovePiece;
-      if (q < per) break;
-      q -= static_cast<int>(per);
-    }
-    uint8_t* dst = ar.base[x] + (seq * slots + to) * ar.bytes[x];
-    const uint8_t* src = ar.base[x] + (seq * slots + from) * ar.bytes[x];
-    const int64_t words = ar.bytes[x] >> ar.shift[x], w0 = static_cast<int64_t>(q) * kMovePiece;
-    switch (ar.shift[x]) {
-      case 4: move_piece(reinterpret_cast<uint4*>(dst), reinterpret_cast<const uint4*>(src), w0, words, lane); break;
-      case 3: move_piece(reinterpret_cast<uint2*>(dst), reinterpret_cast<const uint2*>(src), w0, words, lane); break;
-      case 2: move_piece(reinterpret_cast<uint32_t*>(dst), reinterpret_cast<const uint32_t*>(src), w0, words, lane); break;
-      case 1: move_piece(reinterpret_cast<uint16_t*>(dst), reinterpret_cast<const uint16_t*>(src), w0, words, lane); break;
-      default: move_piece(dst, src, w0, words, lane);
-    }
-  };
   const bool tail = part && keep < n;                       // the incomplete block moves to slot `keep`
   const bool chained = tail && count > 0 && moves[0].y == keep;
-  const int64_t items = static_cast<int64_t>(count) * pieces;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveWarps;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5); it < items + (tail ? tail_pieces : 0); it += step) {
-    if (it < items) {
-      const int64_t m = it / pieces;
-      const int q = static_cast<int>(it - m * pieces);
-      copy(q, moves[m].x, moves[m].y);
-      if (m == 0 && chained) copy(q, keep, n);
-    } else {
-      const int q = static_cast<int>(it - items);
-      if (!chained || q >= pieces) copy(q, keep, n);
+  const int2 tail_move = make_int2(static_cast<int32_t>(keep), static_cast<int32_t>(n));
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kMoveWarps;
+  int64_t it = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  // steps in order: the moves of every array, then the incomplete block's
+  // (unless the lanes of move 0 take it along)
+  for (int x = 0; x < arrays + (tail ? arrays + tail_arrays : 0); ++x) {
+    const bool t = x >= arrays;
+    const int y = t ? x - arrays : x;
+    if (t && chained && y < arrays) continue;
+    const int words = static_cast<int>(ar.bytes[y] >> ar.shift[y]);
+    const int64_t cnt = t ? 1 : count;
+    const int64_t steps = move_steps(words, cnt);
+    const int2* mv = t ? &tail_move : moves;
+    const bool ch = !t && chained;
+    uint8_t* base = ar.base[y] + seq * slots * ar.bytes[y];
+    for (; it < steps; it += warps) {
+      switch (ar.shift[y]) {
+        case 4: move_step(reinterpret_cast<uint4*>(base), words, it, mv, cnt, ch, keep, n, lane); break;
+        case 2: move_step(reinterpret_cast<uint32_t*>(base), words, it, mv, cnt, ch, keep, n, lane); break;
+        default: move_step(base, words, it, mv, cnt, ch, keep, n, lane);
+      }
     }
+    it -= steps;
   }
 }
 

@@ -1214,26 +1214,29 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
   REQUIRE_PTR(acc_out, 8);
   REQUIRE_PTR(pos_out, 4);
   if (pos_count > 0) REQUIRE_PTR(pos, 4);
+  const int64_t most = std::min(keep, n - keep);  // moves of a sequence
   // arrays of which every moved block is copied first, then those of which only the incomplete one is
   sgqa::EvictArrays ar{};
-  int64_t pieces = 0, tail_pieces = 0;  // copied per move, and for the incomplete block
-  for (int i = 0; i < num_arrays; ++i)
+  int full = 0, only_tail = 0;
+  int64_t steps = 0;  // of a sequence, at most
+  for (int i = 0; i < num_arrays; ++i) {
     if (arrays[i].data == nullptr || arrays[i].block_bytes < 1)
       return fail(SGQA_ERR_INVALID_ARGUMENT, "array %d: NULL or without bytes", i);
-  for (int pass = 0, x = 0; pass < 2; ++pass)
-    for (int i = 0; i < num_arrays; ++i) {
-      if ((arrays[i].tail_only != 0) != (pass == 1)) continue;
-      int shift = 4;  // the widest word that address and size allow
-      while (shift > 0 && ((reinterpret_cast<uintptr_t>(arrays[i].data) | static_cast<uintptr_t>(arrays[i].block_bytes)) &
-                           ((1u << shift) - 1)))
-        --shift;
-      ar.base[x] = static_cast<uint8_t*>(arrays[i].data);
-      ar.bytes[x] = arrays[i].block_bytes;
-      ar.shift[x++] = shift;
-      const int64_t n_pieces = ((arrays[i].block_bytes >> shift) + sgqa::kMovePiece - 1) / sgqa::kMovePiece;
-      if (pass == 0) pieces += n_pieces;
-      tail_pieces += n_pieces;
-    }
+    if (arrays[i].block_bytes > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "array %d: blocks of 2 GB or more", i);
+    (arrays[i].tail_only != 0 ? only_tail : full) += 1;
+  }
+  for (int i = 0, x = 0, y = full; i < num_arrays; ++i) {
+    const bool t = arrays[i].tail_only != 0;
+    const int at = t ? y++ : x++;
+    // the widest word that address and size allow
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(arrays[i].data) | static_cast<uintptr_t>(arrays[i].block_bytes);
+    const int shift = bits % 16 == 0 ? 4 : bits % 4 == 0 ? 2 : 0;
+    ar.base[at] = static_cast<uint8_t*>(arrays[i].data);
+    ar.bytes[at] = arrays[i].block_bytes;
+    ar.shift[at] = shift;
+    const int64_t words = arrays[i].block_bytes >> shift;
+    steps += (t ? 0 : sgqa::move_steps(words, most)) + (part ? sgqa::move_steps(words, 1) : 0);
+  }
   const EvictLayout l = evict_layout(num_seqs, slots);
   if ((s = check_ws(workspace, workspace_bytes, l.bytes)) != SGQA_OK) return s;
   if (num_seqs > 65535) return fail(SGQA_ERR_UNSUPPORTED, "at most 65535 sequences per call");
@@ -1245,8 +1248,8 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
   ws.count = ws_at<int32_t>(workspace, l.count_off);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // A cluster per sequence holds up to 131072 blocks (a 1M-token context of
-  // 8-token blocks); about 4096 slots per CTA keep its passes short.
-  const int64_t ncta = std::min<int64_t>(sgqa::kEvMaxCluster, (n + 4095) / 4096);
+  // 8-token blocks); 1024 slots per CTA, one per thread, as long as that lasts.
+  const int64_t ncta = std::min<int64_t>(sgqa::kEvMaxCluster, (n + 1023) / 1024);
   if (n <= static_cast<int64_t>(sgqa::kEvMaxCluster) * sgqa::kEvSlots) {
     const size_t smem = sizeof(sgqa::EvictSmem);
     static_assert(sizeof(sgqa::EvictSmem) <= 232448, "select state exceeds shared memory");
@@ -1273,15 +1276,12 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
         acc, pos, pos_count, evicted, n, part, keep, first, recent, slots, ws, acc_out, pos_out);
     SGQA_LAUNCH_CHECK("evict_select_long_kernel");
   }
-  const int64_t most = std::min(keep, n - keep);  // moves of a sequence
-  if (num_arrays == 0 || keep == n || (most == 0 && !part)) return SGQA_OK;
-  if (pieces + tail_pieces > INT32_MAX) return fail(SGQA_ERR_UNSUPPORTED, "blocks too large");
-  const int64_t items = most * pieces + (part ? tail_pieces : 0);  // at most
-  const int64_t want = (items + sgqa::kMoveWarps - 1) / sgqa::kMoveWarps;
-  const int64_t per_seq = std::min<int64_t>(want, std::max<int64_t>(1, 8 * kSmCount / num_seqs));
+  if (keep == n || steps == 0) return SGQA_OK;
+  // one step per warp: sequences differ in their moves, and the block scheduler
+  // evens that out better than a loop over equal shares
+  const int64_t per_seq = std::min<int64_t>((steps + sgqa::kMoveWarps - 1) / sgqa::kMoveWarps, 65535);
   sgqa::evict_move_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(num_seqs)),
-                            sgqa::kMoveWarps * 32, 0, st>>>(ar, ws, n, part, keep, slots, static_cast<int>(pieces),
-                                                            static_cast<int>(tail_pieces));
+                            sgqa::kMoveWarps * 32, 0, st>>>(ar, full, only_tail, ws, n, part, keep, slots);
   SGQA_LAUNCH_CHECK("evict_move_kernel");
   return SGQA_OK;
 }

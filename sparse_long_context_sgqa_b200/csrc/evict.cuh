@@ -42,26 +42,35 @@ __device__ __forceinline__ uint64_t evict_key(int64_t acc, int32_t pos, int64_t 
   return k == ~0ull ? k - 1 : k;
 }
 
-// Block-wide exclusive scan of two counts (packed); returns this thread's
-// prefix and the totals.
-__device__ __forceinline__ uint2 evict_scan(uint2 v, uint2* warp_tot, uint2& total) {
+// Exclusive scan of two counts per warp over the block's 32 warps: `v` of lane 0
+// counts; every lane gets its warp's prefix, and the totals.
+__device__ __forceinline__ uint2 evict_warp_scan(uint2 v, uint2* warp_tot, uint2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) warp_tot[warp] = v;
+  __syncthreads();
+  const uint2 own = warp_tot[lane];  // every warp scans the 32 totals itself
+  uint2 x = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) { x.x += a; x.y += b; }
+  }
+  total = make_uint2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+  return make_uint2(__shfl_sync(0xffffffffu, x.x - own.x, warp), __shfl_sync(0xffffffffu, x.y - own.y, warp));
+}
+
+// The same per thread.
+__device__ __forceinline__ uint2 evict_scan(uint2 v, uint2* warp_tot, uint2& total) {
+  const int lane = threadIdx.x & 31;
   uint2 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
     if (lane >= o) { x.x += a; x.y += b; }
   }
-  __syncthreads();
-  if (lane == 31) warp_tot[warp] = x;
-  __syncthreads();
-  uint2 before = make_uint2(0, 0), all = make_uint2(0, 0);
-  for (int w = 0; w < kEvictThreads / 32; ++w) {
-    if (w < warp) { before.x += warp_tot[w].x; before.y += warp_tot[w].y; }
-    all.x += warp_tot[w].x;
-    all.y += warp_tot[w].y;
-  }
-  total = all;
+  const uint2 sum = make_uint2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+  const uint2 before = evict_warp_scan(sum, warp_tot, total);
   return make_uint2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
@@ -268,9 +277,9 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   const int cnt = static_cast<int>(max(static_cast<int64_t>(0), min(n, s0 + per) - s0));
   const int64_t* a = acc + seq * slots;
   const int32_t* p = pos + seq * slots;  // read below `known` only
-  // an odd number of slots per thread: 8-byte reads of neighbours fall in distinct banks
-  const int ipt = static_cast<int>((per + kEvictThreads - 1) / kEvictThreads) | 1;
-  const int i0 = min(tid * ipt, cnt), i1 = min(i0 + ipt, cnt);
+  // for the lists: a contiguous range per warp, at most 16 rounds of 32 slots
+  const int its = static_cast<int>((per + kEvictThreads - 1) / kEvictThreads);
+  const int w0 = (tid >> 5) * 32 * its + lane;
   const int64_t tail_acc = part ? a[n] : 0;
   for (int i = tid; i < cnt; i += 4 * kEvictThreads) {  // four loads of each in flight
     int64_t va[4];
@@ -398,17 +407,17 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
       cluster.sync();
       if (rank == 0) {
         const uint32_t c = min(sm.ccount, static_cast<uint32_t>(kEvRank));
-        if (tid < static_cast<int>(c)) {
-          const uint64_t k = sm.ckey[tid];
-          const uint32_t ps = sm.cpos[tid];
+        for (uint32_t x = tid >> 5; x < c; x += kEvictThreads / 32) {  // a warp counts who stands before x
+          const uint64_t k = sm.ckey[x];
+          const uint32_t ps = sm.cpos[x];
           uint32_t better = 0;
-#pragma unroll 8
-          for (uint32_t i = 0; i < c; ++i) {
+          for (uint32_t i = lane; i < c; i += 32) {
             const uint64_t ki = sm.ckey[i];
             const uint32_t pi = sm.cpos[i];
-            better += (ki > k || (ki == k && (pi < ps || (pi == ps && i < static_cast<uint32_t>(tid))))) ? 1u : 0u;
+            better += (ki > k || (ki == k && (pi < ps || (pi == ps && i < x)))) ? 1u : 0u;
           }
-          if (better == need - 1) {
+          better = __reduce_add_sync(0xffffffffu, better);
+          if (lane == 0 && better == need - 1) {
             sm.tkey = k;
             sm.tpos = ps;
           }
@@ -425,14 +434,15 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   };
   // freed slots below `keep`, kept blocks behind it: ranks over the whole sequence
   uint2 mine = make_uint2(0, 0), tot;
-  uint32_t keeps = 0;  // bit i: kept (ipt <= 17)
-  for (int i = i0; i < i1; ++i) {
-    const bool k = kept(i);
-    keeps |= (k ? 1u : 0u) << (i - i0);
-    if (s0 + i < keep) mine.x += !k;
-    else mine.y += k;
+  uint32_t keeps = 0;  // bit t: round t's slot is kept
+  for (int t = 0; t < its; ++t) {
+    const int i = w0 + 32 * t;
+    const bool in = i < cnt, k = in && kept(i), below = in && s0 + i < keep;
+    keeps |= (k ? 1u : 0u) << t;
+    mine.x += __popc(__ballot_sync(0xffffffffu, below && !k));
+    mine.y += __popc(__ballot_sync(0xffffffffu, k && !below));
   }
-  uint2 at = evict_scan(mine, sm.warp_tot, tot);
+  uint2 at = evict_warp_scan(mine, sm.warp_tot, tot);  // of this warp
   if (tid == 0) sm.sums = tot;
   cluster.sync();
   uint2 all = make_uint2(0, 0);
@@ -450,16 +460,21 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   int2* moves = ws.moves + seq * ws.cap;
   int64_t* macc = ws.moved_acc + seq * (ws.cap + 1);
   int32_t* mpos = ws.moved_pos + seq * ws.cap;
+  const uint32_t lt = (1u << lane) - 1u;
   uint2 r = at;
-  for (int i = i0; i < i1; ++i) {
-    const bool k = (keeps >> (i - i0)) & 1u;
-    if (s0 + i < keep) {
-      if (!k) moves[r.x++].x = static_cast<int32_t>(s0 + i);
-    } else if (k) {
-      moves[r.y].y = static_cast<int32_t>(s0 + i);
-      macc[r.y] = sm.acc[i];
-      mpos[r.y++] = sm.pos[i];
+  for (int t = 0; t < its; ++t) {
+    const int i = w0 + 32 * t;
+    const bool in = i < cnt, k = (keeps >> t) & 1u, below = in && s0 + i < keep;
+    const uint32_t free_slots = __ballot_sync(0xffffffffu, below && !k), late = __ballot_sync(0xffffffffu, k && !below);
+    if (below && !k) moves[r.x + __popc(free_slots & lt)].x = static_cast<int32_t>(s0 + i);
+    if (k && !below) {
+      const uint32_t to = r.y + __popc(late & lt);
+      moves[to].y = static_cast<int32_t>(s0 + i);
+      macc[to] = sm.acc[i];
+      mpos[to] = sm.pos[i];
     }
+    r.x += __popc(free_slots);
+    r.y += __popc(late);
   }
   if (tid == 0 && rank == 0) {
     if (all.x != all.y) report(kDevBounds);  // original numbers that occur twice
@@ -471,19 +486,17 @@ evict_select_kernel(const int64_t* acc, const int32_t* pos, int64_t known, int64
   int64_t* ao = acc_out + seq * slots;
   int32_t* po = pos_out + seq * slots;
   uint32_t hole = at.x;
-  for (int i = i0; i < i1 && s0 + i < keep; ++i) {
-    if (!((keeps >> (i - i0)) & 1u)) {
-      const bool ok = hole < all.y;
-      sm.acc[i] = ok ? macc[hole] : 0;
-      sm.pos[i] = ok ? mpos[hole] : -1;
-      ++hole;
+#pragma unroll 4
+  for (int t = 0; t < its; ++t) {
+    const int i = w0 + 32 * t;
+    const bool k = (keeps >> t) & 1u, below = i < cnt && s0 + i < keep;
+    const uint32_t free_slots = __ballot_sync(0xffffffffu, below && !k);
+    if (below) {
+      const uint32_t h = hole + __popc(free_slots & lt);
+      ao[s0 + i] = k ? sm.acc[i] : h < all.y ? macc[h] : 0;
+      po[s0 + i] = k ? sm.pos[i] : h < all.y ? mpos[h] : -1;
     }
-  }
-  __syncthreads();
-  const int below = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(cnt), keep - s0)));
-  for (int i = tid; i < below; i += kEvictThreads) {
-    ao[s0 + i] = sm.acc[i];
-    po[s0 + i] = sm.pos[i];
+    hole += __popc(free_slots);
   }
   for (int64_t s = keep + static_cast<int64_t>(rank) * kEvictThreads + tid; s < slots; s += static_cast<int64_t>(ncta) * kEvictThreads)
     ao[s] = s == keep && part ? tail_acc : 0;

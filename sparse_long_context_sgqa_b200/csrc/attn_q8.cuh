@@ -872,11 +872,10 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
     // ---------------------------------------------------------------- softmax + epilogue
     tc::regs_inc<kQpRegsMany>();
     // Two warps per TMEM lane quadrant take alternate tiles (`half`: which), so that
-    // one's exponentials run beside the other's loads and stores.  A tile's weights
-    // are computed with the row's reference as this warp knows it; before they
-    // count, the other warp's decision on the tile before is picked up (bar.sync;
-    // published by bar.arrive), and where a reference moved, or has to, they are
-    // computed once more.  A failed wait clears `ok` but keeps every barrier step.
+    // one's exponentials run beside the other's loads and stores.  The rows'
+    // reference goes from tile to tile through shared memory (bar.arrive, bar.sync);
+    // where a tile's weights show that it has to move, they are computed once more.
+    // A failed wait clears `ok` but keeps every barrier step in place.
     const int quad = warp & 3, half = (warp - 8) >> 2;
     const int pair_bar = 1 + quad;
     const int pub_mine = 5 + 2 * quad + half, pub_other = 5 + 2 * quad + (half ^ 1);
@@ -1010,6 +1009,12 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         // P buffer b is free once O += P(j-2) V(j-2) has read it
         if (j >= 2) ok = ok && tc::mbar_wait(bar(sm.pv_done[b]), ((j / 2) - 1) & 1, abort);
         tc::fence_after();
+        // The reference after tile j-1, from the other warp.  Waiting for it here
+        // lets the two warps' exponentials take turns (one sub-partition's).
+        if (j > 0) {
+          asm volatile("bar.sync %0, 64;" ::"r"(pub_other) : "memory");
+          ref = sm.mchain[m];
+        }
         float ls;
         for (int pass = 0; pass < 2; ++pass) {
           const float neg = ref == -INFINITY ? 0.f : -ref;
@@ -1050,17 +1055,9 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
             tc::tmem_st16(tP + 16 * h, pk);
           }
           if (pass == 1) break;
-          // The reference after tile j-1, from the other warp.  These weights stand
-          // unless it moved, a weight is above 2^15, or the row had none yet.
-          float m_prev = -INFINITY;
-          if (j > 0) {
-            asm volatile("bar.sync %0, 64;" ::"r"(pub_other) : "memory");
-            m_prev = sm.mchain[m];
-          }
-          const bool moved = m_prev != ref;
+          // these weights stand unless one is above 2^15, or the row has no reference yet
           const bool high = __half2float(__hmax(__low2half(top), __high2half(top))) > 40000.f || (ref == -INFINITY && (use[0] | use[1]) != 0u);
-          if (!__any_sync(0xffffffffu, moved || high)) break;
-          ref = m_prev;
+          if (!__any_sync(0xffffffffu, high)) break;
           float mx = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -1074,9 +1071,10 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
           // down to 2^-18 of it in full and resolves 2^-28 of it, and the reference
           // stays until the scores grow by 2^11.
           const bool need = mx > ref + 15.f;
+          const float old = ref;
           if (need) ref = mx - 4.f;
           if (j > 0 && __any_sync(0xffffffffu, need)) {
-            const float alpha = need ? exp2f(m_prev - ref) : 1.f;
+            const float alpha = need ? exp2f(old - ref) : 1.f;
             // O must hold P(j-1) V(j-1) before it is rescaled.  (This warp knows the
             // product of tile j-2 done, so tile j-3's too: the phase is tile j-1's.)
             ok = ok && tc::mbar_wait(bar(sm.pv_done[b ^ 1]), ((j - 1) / 2) & 1, abort);

@@ -948,7 +948,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       const uint32_t use[2] = {last ? 1u << (8 * (t / 8 - cb)) : (mb_next.x >> qs) & 0x01010101u,
                                last ? 0u : (mb_next.y >> qs) & 0x01010101u};
       if (j + 2 < n_union_tiles) mb_next = *reinterpret_cast<const uint2*>(umask + 8 * (j + 2));
-      if (!last) ok = ok && tc::mbar_wait(bar(sm.meta_full[slot]), (j / (4 * kQpMeta)) & 1, abort);
+      if (!last && (j & 3) < 2) ok = ok && tc::mbar_wait(bar(sm.meta_full[slot]), (j / (4 * kQpMeta)) & 1, abort);
       const float4* meta = last ? sm.meta_cur : &sm.meta[slot][at];
       if (const uint32_t nan = (sm.meta_nan[slot] >> at) & 0xFFu) {  // rare
         const uint32_t nk = sm.meta_nan_k[slot] >> at;
@@ -1018,7 +1018,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         float ls;
         for (int pass = 0; pass < 2; ++pass) {
           const float neg = ref == -INFINITY ? 0.f : -ref;
-          __half2 top = __float2half2_rn(0.f);
+          float top = 0.f;  // largest sum of a block's weights
           ls = 0.f;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1043,20 +1043,21 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
                     pk[4 * e + x] = pack_f16x2(p0, p1);
                   }
                   const uint64_t sum = add_f32x2(add_f32x2(pe[0], pe[1]), add_f32x2(pe[2], pe[3]));
-                  ls = fmaf(f32x2_lo(sum) + f32x2_hi(sum), mt.z, ls);
+                  const float bs = f32x2_lo(sum) + f32x2_hi(sum);
+                  top = fmaxf(top, bs);
+                  ls = fmaf(bs, mt.z, ls);
                 }
               } else {
 #pragma unroll
                 for (int x = 4 * e2; x < 4 * e2 + 8; ++x) pk[x] = 0u;
               }
             }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) top = __hmax2(top, *reinterpret_cast<__half2*>(&pk[x]));
             tc::tmem_st16(tP + 16 * h, pk);
           }
           if (pass == 1) break;
-          // these weights stand unless one is above 2^15, or the row has no reference yet
-          const bool high = __half2float(__hmax(__low2half(top), __high2half(top))) > 40000.f || (ref == -INFINITY && (use[0] | use[1]) != 0u);
+          // these weights stand unless a block's sum leaves FP16's range (one of its
+          // weights is above 2^12 then), or the row has no reference yet
+          const bool high = top > 60000.f || (ref == -INFINITY && (use[0] | use[1]) != 0u);
           if (!__any_sync(0xffffffffu, high)) break;
           float mx = -INFINITY;
 #pragma unroll
@@ -1069,8 +1070,8 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
           }
           // A new reference lies 4 below the largest weight: FP16 then holds weights
           // down to 2^-18 of it in full and resolves 2^-28 of it, and the reference
-          // stays until the scores grow by 2^11.
-          const bool need = mx > ref + 15.f;
+          // stays until the scores grow by 2^8 at least.
+          const bool need = mx > ref + 12.f;
           const float old = ref;
           if (need) ref = mx - 4.f;
           if (j > 0 && __any_sync(0xffffffffu, need)) {

@@ -595,15 +595,15 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 //               range of 16 bits: where one token takes most of a row (a sink), the
 //               result lies in weights 2^-14 of the largest and below, which two
 //               E4M3 halves in one accumulator lose.
-// lo is not multiplied by 16 here (both halves add into one accumulator): it
-// resolves 2^-10 below a row's largest query value of 224 .. 448.
+// lo is not multiplied by 16 here (both halves add into one accumulator): a query
+// value is exact down to 2^-11 of the row's largest, smaller ones are off by at most
+// 2^-19 of it.
 // A block's K scale and the row's query scale multiply its scores; its V scale
 // enters the exponent (2^(s + log2 vs - ref)) and leaves the block's sum again.
 //
 // WEIGHTS: the second sweep of a call that accumulates weights.  With every
-// row's log-sum known, S alone is computed again, the halves in buffers of
-// their own (lo times 16), and each block's weights are summed over the unit's
-// 128 rows, eight blocks of a tile at a time.
+// row's log-sum known, S alone is computed again, and each block's weights are
+// summed over the unit's 128 rows, eight blocks of a tile at a time.
 // ---------------------------------------------------------------------------
 constexpr int kQpStages = 8;      // K ring depth, 12 KB each
 constexpr int kQpVStages = 4;     // V ring depth (codes)
@@ -694,8 +694,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
   tc::fence_after();
   const uint32_t tmem = sm.tmem;
   const uint32_t tO = tmem;                              // columns [0, 192)
-  const uint32_t tS0 = WEIGHTS ? tmem : tmem + 192;      // S buffers: 64 columns each; WEIGHTS: hi 64, lo 64
-  constexpr uint32_t kSBuf = WEIGHTS ? 128 : 64;
+  const uint32_t tS0 = tmem + 192;                       // S buffers of 64 columns
   const uint32_t tP0 = tmem + 320;                       // P buffers [320, 352), [352, 384), two FP16 per column
   const uint32_t tQ = tmem + 384;                        // Q: hi [384, 432), lo [432, 480)
   int issued = 0;
@@ -798,8 +797,8 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int kk = 0; kk < 6; ++kk)  // Q: 8 columns per 32 dims; K: +512 B per 64 dims, +32 B per 32
-                tc::mma_f8_tmem_a(tS0 + kSBuf * b + (WEIGHTS ? 64 * half : 0), tQ + 48 * half + 8 * kk,
-                                  dk + (kk >> 1) * 32 + (kk & 1) * 2, id_qk, (kk > 0 || (!WEIGHTS && half > 0)) ? 1u : 0u);
+                tc::mma_f8_tmem_a(tS0 + 64 * b, tQ + 48 * half + 8 * kk,
+                                  dk + (kk >> 1) * 32 + (kk & 1) * 2, id_qk, (kk > 0 || half > 0) ? 1u : 0u);
             tc::mma_commit(bar(sm.k_empty[s]));
             tc::mma_commit(bar(sm.s_full[b]));
           }
@@ -918,8 +917,8 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         for (int x = 0; x < 8; ++x) {
           const uint32_t a = w[16 * c + 2 * x], b = w[16 * c + 2 * x + 1];
           uint32_t ha, la, hb, lb;
-          split_e4m3(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv, ha, la, WEIGHTS ? 16.f : 1.f);
-          split_e4m3(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv, hb, lb, WEIGHTS ? 16.f : 1.f);
+          split_e4m3(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xFFFF0000u) * inv, ha, la, 1.f);
+          split_e4m3(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv, hb, lb, 1.f);
           h8[x] = ha | (hb << 16);
           l8[x] = la | (lb << 16);
         }
@@ -942,7 +941,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       const int b = half;
       const bool last = j >= n_union_tiles;  // the current-block tile
       const int slot = last ? kQpMeta : (j / 4) % kQpMeta, at = last ? 0 : 8 * (j & 3);
-      const uint32_t tS = tS0 + kSBuf * b + lane_off, tP = tP0 + 32 * b + lane_off;
+      const uint32_t tS = tS0 + 64 * b + lane_off, tP = tP0 + 32 * b + lane_off;
       // bit 8 e of word h: the row's query attends block 4 h + e (the plan's bytes
       // behind the union are zeros)
       const uint32_t use[2] = {last ? 1u << (8 * (t / 8 - cb)) : (mb_next.x >> qs) & 0x01010101u,
@@ -971,38 +970,36 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
           if (x > end && ((use[0] >> (8 * (x >> 3))) & 1u)) sr[x] = __float_as_uint(-INFINITY);
       }
       if constexpr (WEIGHTS) {
+        tc::fence_before();
+        tc::mbar_arrive(bar(sm.s_free[b]));
         // weights of the row, summed by block, then over the warp's 32 rows: lane
-        // 4 i + e ends with block e of its half
+        // 8 i + e ends with block e
+        float w[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t lo[32];
-          tc::tmem_ld32(tS + 64 + 32 * h, lo);
-          tc::tmem_ld_wait();
-          if (h == 1) {
-            tc::fence_before();
-            tc::mbar_arrive(bar(sm.s_free[b]));
+        for (int e = 0; e < 8; ++e) {
+          const float cf = meta[e].x * rc;
+          const uint64_t c2 = pack_f32x2(cf, cf), o2 = pack_f32x2(-row_lse, -row_lse);
+          uint64_t p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint64_t v = fma_f32x2(pack_f32x2(__uint_as_float(sr[8 * e + 2 * x]), __uint_as_float(sr[8 * e + 2 * x + 1])), c2, o2);
+            p[x] = pack_f32x2(fast_exp2(f32x2_lo(v)), fast_exp2(f32x2_hi(v)));
           }
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float cf = meta[4 * h + e].x * rc;
-            float p[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              p[x] = fast_exp2(fmaf(fmaf(__uint_as_float(lo[8 * e + x]), 0.0625f, __uint_as_float(sr[32 * h + 8 * e + x])), cf, -row_lse));
-            w[e] = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-            if (!((use[h] >> (8 * e)) & 1u) || !(w[e] == w[e])) w[e] = 0.f;
-          }
-          float z[2];
-          const bool h2 = lane & 2, h1 = lane & 1;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) z[c] = (h2 ? w[2 + c] : w[c]) + __shfl_xor_sync(0xffffffffu, h2 ? w[c] : w[2 + c], 2);
-          float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane < 4 && v > 0.f)
-            acc_add(acc + seq * blocks + (last ? static_cast<int32_t>(cb) + lane : sm.ids[slot][at + 4 * h + lane]), v);
+          const uint64_t sum = add_f32x2(add_f32x2(p[0], p[1]), add_f32x2(p[2], p[3]));
+          w[e] = f32x2_lo(sum) + f32x2_hi(sum);
+          if (!((use[e >> 2] >> (8 * (e & 3))) & 1u) || !(w[e] == w[e])) w[e] = 0.f;
         }
+        float y[4], z[2];
+        const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = (h4 ? w[4 + c] : w[c]) + __shfl_xor_sync(0xffffffffu, h4 ? w[c] : w[4 + c], 4);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) z[c] = (h2 ? y[2 + c] : y[c]) + __shfl_xor_sync(0xffffffffu, h2 ? y[c] : y[2 + c], 2);
+        float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (lane < 8 && v > 0.f)
+          acc_add(acc + seq * blocks + (last ? static_cast<int32_t>(cb) + lane : sm.ids[slot][at + lane]), v);
       } else {
         tc::fence_before();
         tc::mbar_arrive(bar(sm.s_free[b]));

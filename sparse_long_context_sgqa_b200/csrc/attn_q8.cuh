@@ -78,7 +78,7 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
 //                           computed twice are not read); P through shared memory,
 //                           columns 16 heads' first, second and third E5M2 values
 // A token's scores never cross threads for a maximum: the reference moves only
-// when some weight exceeds 2^15 (one barrier-or per tile tells), and only then
+// when some weight exceeds 2^14 (one barrier-or per tile tells), and only then
 // are a head's maxima reduced over the tile and O rescaled in TMEM.
 // K and V are gathered by a warp each (16 lanes, one 1.5 KB box per block) into
 // rings of their own: a K stage is free again after its MMA, a V stage only
@@ -369,9 +369,10 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       for (int h = 0; h < 8; ++h) {
         const float v = fmaf(__uint_as_float(sl[h]), 0.0625f, __uint_as_float(sh[h])) * (sc.x * rc[h]);
         x[h] = use ? v : -INFINITY;
-        grow = grow || x[h] + lvs > ref[h] + 15.f;
+        grow = grow || x[h] + lvs > ref[h] + 14.f;
       }
-      // does any weight of the tile exceed 2^15?
+      // does any weight of the tile exceed 2^14?  (2^15 with a V scale between two
+      // powers of two: still in FP16's range)
       int any;
       asm volatile(
           "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.s32 %0, 1, 0, q;\n}"
@@ -380,7 +381,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
           : "memory");
       if (any) {
         // new references: the largest score (plus log2 of its V scale) - 4, so that
-        // they stay until the scores grow by 2^11
+        // they stay until the scores grow by 2^10
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const int v = __float_as_int(fmaxf(x[h] + lvs, -INFINITY));
@@ -392,7 +393,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           const float mx = fmaxf(fmaxf(sm.wmax[0][h0 + h], sm.wmax[1][h0 + h]), fmaxf(sm.wmax[2][h0 + h], sm.wmax[3][h0 + h]));
-          const float nr = mx > ref[h] + 15.f ? mx - 4.f : ref[h];
+          const float nr = mx > ref[h] + 14.f ? mx - 4.f : ref[h];
           al[h] = nr == ref[h] ? 1.f : exp2f(ref[h] - nr);
           ref[h] = nr;
           l[h] *= al[h];
@@ -998,8 +999,11 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (lane < 8 && v > 0.f)
-          acc_add(acc + seq * blocks + (last ? static_cast<int32_t>(cb) + lane : sm.ids[slot][at + lane]), v);
+        // (after a wait that gave up the block numbers may never have been written)
+        if (ok && lane < 8 && v > 0.f) {
+          const int64_t id = last ? cb + lane : sm.ids[slot][at + lane];
+          if (id >= 0 && id < blocks) acc_add(acc + seq * blocks + id, v);
+        }
       } else {
         tc::fence_before();
         tc::mbar_arrive(bar(sm.s_free[b]));

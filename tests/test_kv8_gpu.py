@@ -250,6 +250,50 @@ def test_attention_blocks_of_very_different_scale(Bd, cuda_device, nq):
     check_attn(c, run_attn(Bd, c), ref, tol)
 
 
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_scales_between_powers_of_two(Bd, cuda_device, nq):
+    c = make_attn(2, 2, nq, 1500, 120, cuda_device, sigma=3.0)
+    c["sc"] *= torch.rand(c["sc"].shape, generator=gen(8)).to(cuda_device) + 1
+    ref, tol, weights = reference(c)
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    check_attn(c, run_attn(Bd, c, acc=acc), ref, tol)
+    check_weights(acc, 0, weights, nq * 2 * 2)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_of_queries_with_infinities(Bd, cuda_device, nq):
+    c = make_attn(1, 2, nq, 500, 40, cuda_device)
+    bad = c["q"].clone()
+    bad[0, 0, 3, 7], bad[0, nq - 1, 20, 100] = float("inf"), float("nan")
+    fine = run_attn(Bd, c)
+    c["q"] = bad
+    acc = torch.zeros((1, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    got = run_attn(Bd, c, acc=acc)
+    assert torch.isnan(got[0, 0, 3]).all() and torch.isnan(got[0, nq - 1, 20]).all()
+    same = torch.ones(got.shape[:3], dtype=torch.bool, device=cuda_device)
+    same[0, 0, 3] = same[0, nq - 1, 20] = False
+    assert torch.equal(got[same], fine[same])
+    # the other heads' weights are counted
+    assert abs(float(acc.double().sum()) * R.UNIT - (nq * 2 * HG - 2)) < 1e-3
+
+
+@pytest.mark.parametrize("nq", [1, 64])
+def test_a_wait_that_runs_out_is_reported_and_later_calls_succeed(Bd, cuda_device, nq):
+    c = make_attn(2, 4, nq, 3000, 256, cuda_device)
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    first = run_attn(Bd, c, acc=acc)
+    once = acc.clone()
+    try:
+        Bd.sgqa_set_wait_limit_ns(1)
+        with pytest.raises(Bd.SgqaError) as e:
+            run_attn(Bd, c, acc=acc)
+    finally:
+        Bd.sgqa_set_wait_limit_ns(0)
+    assert e.value.code == 5
+    acc.zero_()
+    assert torch.equal(run_attn(Bd, c, acc=acc), first) and torch.equal(acc, once)
+
+
 @pytest.mark.parametrize("nq", [2, 40])
 def test_nan_blocks_reach_only_who_attends_them(Bd, cuda_device, nq):
     c = make_attn(2, 2, nq, 1000, 50, cuda_device)

@@ -163,28 +163,12 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
     if (b >= cnt) return -1;
     return id < 0 || id >= hist || id <= prev ? -2 : id;
   };
-  if (threadIdx.x == 0) {
-    sm.abort = 0;
-    for (int s = 0; s < kQdStages; ++s) {
-      tc::mbar_init(bar(sm.k_full[s]), kQdTile);
-      tc::mbar_init(bar(sm.v_full[s]), kQdTile);
-      tc::mbar_init(bar(sm.k_empty[s]), 1);
-      tc::mbar_init(bar(sm.v_empty[s]), 1);
-    }
-    for (int s = 0; s < kQdMeta; ++s) tc::mbar_init(bar(sm.meta_full[s]), kQdTile);
-    for (int b = 0; b < kQdS; ++b) {
-      tc::mbar_init(bar(sm.s_full[b]), 1);
-      tc::mbar_init(bar(sm.s_free[b]), 256);
-    }
-    for (int b = 0; b < 2; ++b) tc::mbar_init(bar(sm.drain[b]), 1);
-    tc::mbar_init(bar(sm.p_full), 256);
-    tc::mbar_init(bar(sm.pv_done), 1);
-    tc::mbar_init(bar(sm.q_full), 256);
-    tc::mbar_init(bar(sm.o_final), 1);
-    tc::mbar_fence_init();
-  }
-  // the producers' first ids, before the barrier
-  int id1 = -1, prev1 = -1, id2 = -1, prev2 = -1, cnt = 0;
+  int issued = 0;  // producers: tiles whose copies this warp issued
+  const bool is_k = warp == 0;
+  // ids and their predecessors are fetched two tiles ahead, scales one
+  int id2 = -1, prev2 = -1, cnt = 0;
+  int32_t blk = -1;
+  float2 sc = make_float2(0.f, 1.f);
   auto fetch = [&](int j, int& id, int& prev) {
     const int b = b0 + j * kQdTile + lane;
     id = prev = -1;
@@ -193,10 +177,63 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       if (b > 0) prev = __ldg(ids + b - 1);
     }
   };
+  auto resolve = [&](int j, int id, int prev) -> int32_t {
+    const int32_t r = block_at(lane < kQdTile ? b0 + j * kQdTile + lane : b1, cnt, id, prev);
+    if (r == -2 && is_k) report(kDevBounds);
+    return r;
+  };
+  auto scales = [&](int32_t x) -> float2 {
+    return is_k && x >= 0 ? __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + x) * G + g)
+                          : make_float2(0.f, 1.f);
+  };
+  auto copy = [&](int s) {  // this lane's block into stage s; no block: a box outside the cache, filled with zeros
+    const uint32_t full = bar(is_k ? sm.k_full[s] : sm.v_full[s]);
+    tc::mbar_expect_tx(full, kQ8Half);
+    tc::tma_load_5d(smem_u32(is_k ? &sm.k[s][lane][0][0][0] : &sm.v[s][lane][0][0][0]), &kvmap, 0, is_k ? 0 : kQ8Tok, 0,
+                    blk >= 0 ? g : 0, blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
+  };
   if (warp == 0 || warp == 11) {
+    // Each producer sets up its own barriers and sends its first tile off before
+    // the CTA-wide set-up is through.
+    int id1, prev1;
     fetch(0, id1, prev1);
     fetch(1, id2, prev2);
     cnt = min(max(__ldg(sel_count + row), 0), k);
+    if (lane == 0) {
+      tc::prefetch_tmap(&kvmap);
+      for (int s = 0; s < kQdStages; ++s) {
+        tc::mbar_init(bar(is_k ? sm.k_full[s] : sm.v_full[s]), kQdTile);
+        tc::mbar_init(bar(is_k ? sm.k_empty[s] : sm.v_empty[s]), 1);
+      }
+      if (is_k)
+        for (int s = 0; s < kQdMeta; ++s) tc::mbar_init(bar(sm.meta_full[s]), kQdTile);
+      tc::mbar_fence_init();
+    }
+    __syncwarp();
+    blk = resolve(0, id1, prev1);
+    sc = scales(blk);
+    if (n_tiles > 0) {
+      if (lane < kQdTile) copy(0);
+      issued = 1;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    tc::tmem_alloc(smem_u32(&sm.tmem), kQdCols);
+  } else if (warp == 10) {
+    if (lane == 0) {
+      sm.abort = 0;
+      for (int b = 0; b < kQdS; ++b) {
+        tc::mbar_init(bar(sm.s_full[b]), 1);
+        tc::mbar_init(bar(sm.s_free[b]), 256);
+      }
+      for (int b = 0; b < 2; ++b) tc::mbar_init(bar(sm.drain[b]), 1);
+      tc::mbar_init(bar(sm.p_full), 256);
+      tc::mbar_init(bar(sm.pv_done), 1);
+      tc::mbar_init(bar(sm.q_full), 256);
+      tc::mbar_init(bar(sm.o_final), 1);
+      tc::mbar_fence_init();
+    }
+    __syncwarp();
   }
   // the softmax warps' queries: a warp packs two heads, a lane dims 2 lane and
   // 2 lane + 1 of every chunk
@@ -208,11 +245,9 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 #pragma unroll
       for (int c = 0; c < 3; ++c) qw[hh][c] = __ldg(reinterpret_cast<const uint32_t*>(q + (row * kHg + qh + hh) * kD) + 32 * c + lane);
   }
-  if (warp == 1) tc::tmem_alloc(smem_u32(&sm.tmem), kQdCols);
   __syncthreads();
   tc::fence_after();
   const uint32_t tS = sm.tmem, tO = sm.tmem + 32 * kQdS;
-  int issued = 0;  // producers: tiles whose copies this warp issued
 
   // per-head state of the softmax threads
   float ref[8], l[8];
@@ -221,29 +256,11 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 
   if (warp == 0 || warp == 11) {
     // ---------------------------------------------------------------- producers
-    const bool is_k = warp == 0;
-    if (lane == 0) tc::prefetch_tmap(&kvmap);
-    // ids are fetched two tiles ahead, scales one
-    auto resolve = [&](int j, int id, int prev) -> int32_t {
-      int32_t blk = block_at(lane < kQdTile ? b0 + j * kQdTile + lane : b1, cnt, id, prev);
-      if (blk == -2 && is_k) report(kDevBounds);
-      return blk;
-    };
-    auto scales = [&](int32_t blk) -> float2 {
-      return is_k && blk >= 0 ? __ldg(reinterpret_cast<const float2*>(kv_scale) + (seq * blocks + blk) * G + g)
-                              : make_float2(0.f, 1.f);
-    };
-    int32_t blk = resolve(0, id1, prev1);
-    float2 sc = scales(blk);
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % kQdStages;
       if (j >= kQdStages && !tc::warp_wait(bar(is_k ? sm.k_empty[s] : sm.v_empty[s]), ((j / kQdStages) - 1) & 1, abort)) break;
       if (lane < kQdTile) {
-        const uint32_t full = bar(is_k ? sm.k_full[s] : sm.v_full[s]);
-        tc::mbar_expect_tx(full, kQ8Half);
-        // no block: a box outside the cache, filled with zeros
-        tc::tma_load_5d(smem_u32(is_k ? &sm.k[s][lane][0][0][0] : &sm.v[s][lane][0][0][0]), &kvmap, 0, is_k ? 0 : kQ8Tok, 0,
-                        blk >= 0 ? g : 0, blk >= 0 ? static_cast<int32_t>(seq * blocks + blk) : -1, full);
+        if (j > 0) copy(s);
         if (is_k) {
           const int32_t m = blk < 0 ? 0 : blk == hist ? (2 << (t % kQ8Tok)) - 1 : 0xFF;
           const int32_t e = blk < 0 || !isfinite(sc.y) ? 0 : static_cast<int32_t>(__float_as_uint(sc.y) >> 23) - 127;

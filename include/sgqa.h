@@ -255,7 +255,9 @@ sgqa_status sgqa_sparse_attn_paged(const sgqa_params* p, int64_t num_seqs, int64
  * with one FP32 scale for the eight tokens of a block in one group's K (and
  * one for its V); half the bytes of the BF16 caches, for the cache's size and
  * for the decode gather.  block_size 8 only (others return
- * SGQA_ERR_UNSUPPORTED); cache_cap is a multiple of 8.
+ * SGQA_ERR_UNSUPPORTED); cache_cap is a multiple of 8.  The kernels' shared
+ * memory is set up by the first call per device and process (these calls and
+ * sgqa_evict are not supported after cudaDeviceReset()).
  *
  * kv8      : [S, cache_cap / 8, G, 2 (K, V), 8 tokens, D] uint8 E4M3 codes
  *            (16-byte aligned): one group's K and V of a block are contiguous
@@ -285,9 +287,10 @@ sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t ca
 /*
  * sgqa_sparse_attn_gated over the 8-bit cache.  Attention of the values
  * code * scale: a query's current block has one scale for all of its tokens
- * that are in the cache, the query's later ones among them.  Query and softmax
- * weights are not rounded to 8 bits (each is carried as a sum of two E4M3
- * values); sums and softmax statistics are FP32.
+ * that are in the cache, the query's later ones among them.  Queries and softmax
+ * weights are not rounded to 8 bits: a query value is carried as two E4M3 values
+ * (exact down to 2^-11 of its head's largest), a weight to 2^-9 of itself and
+ * down to 2^-27 of the row's largest.  Sums and softmax statistics are FP32.
  *
  * gate : [S, nq, G*Hg] bf16 gate logits, or NULL (no gate)
  * acc  : [S, cache_cap / 8] int64, or NULL.  Accumulated attention weight of

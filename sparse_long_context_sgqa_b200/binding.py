@@ -62,9 +62,17 @@ class Params:
     merge_in_f32: int = 0
     scale: float = 0.0
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_struct", None)  # built again by the next call
+
     def c(self) -> _Params:
-        return _Params(self.num_kv_groups, self.heads_per_group, self.head_dim, self.idx_heads, self.idx_dim,
-                       self.block_size, self.topk, self.merge_in_f32, self.scale)
+        c = self.__dict__.get("_struct")
+        if c is None:
+            c = _Params(self.num_kv_groups, self.heads_per_group, self.head_dim, self.idx_heads, self.idx_dim,
+                        self.block_size, self.topk, self.merge_in_f32, self.scale)
+            self.__dict__["_struct"] = c
+        return c
 
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
@@ -319,18 +327,17 @@ def sgqa_evict(p: Params, num_seqs, cache_cap, cache_len, keep, first, recent, a
     """Keep the `keep` heaviest blocks of every sequence.  arrays: contiguous tensors whose leading dimensions are
     (sequence, block) or (sequence, token); tail_arrays: the same, of which only the incomplete block moves."""
     blocks = num_seqs * (cache_cap // p.block_size)
-    every = []
-    for group, tail in ((arrays, 0), (tail_arrays, 1)):
-        for t in group:
-            size = t.numel() * t.element_size()
-            if not t.is_cuda or not t.is_contiguous() or blocks == 0 or size % blocks:
-                raise ValueError("evict: every array is a contiguous CUDA tensor of cache_cap / block_size blocks per sequence")
-            every.append(_CacheArray(t.data_ptr(), size // blocks, tail))
-    c = (_CacheArray * max(1, len(every)))(*every)
+    n = len(arrays) + len(tail_arrays)
+    c = (_CacheArray * max(1, n))()
+    for i, t in enumerate((*arrays, *tail_arrays) if tail_arrays else arrays):
+        size = t.nbytes
+        if not t.is_cuda or not t.is_contiguous() or blocks == 0 or size % blocks:
+            raise ValueError("evict: every array is a contiguous CUDA tensor of cache_cap / block_size blocks per sequence")
+        c[i] = (t.data_ptr(), size // blocks, i >= len(arrays))
     _run(_lib.sgqa_evict, acc, stream, ctypes.byref(p.c()), num_seqs, cache_cap, cache_len, keep, first, recent,
          _check("acc", acc, torch.int64, blocks), None if pos is None else _check("pos", pos, torch.int32, blocks),
          pos_count, evicted, _check("acc_out", acc_out, torch.int64, blocks), _check("pos_out", pos_out, torch.int32, blocks),
-         c, len(every), *_workspace(workspace))
+         c, n, *_workspace(workspace))
 
 
 def sgqa_set_wait_limit_ns(ns: int):

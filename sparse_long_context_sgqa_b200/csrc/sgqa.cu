@@ -640,6 +640,21 @@ sgqa_status do_attn(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, con
   return do_attn_kv(p, S, q0, nq, q, kv, sel, sel_count, out, gate, ws, st);
 }
 
+// Dynamic shared memory a kernel may use, raised once per device and kernel
+// (`done`: a bit per device) rather than on every call.
+template <typename K>
+sgqa_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return SGQA_OK;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared memory)");
+  done.fetch_or(bit, std::memory_order_release);
+  return SGQA_OK;
+}
+
 // ---- the 8-bit K/V cache ---------------------------------------------------
 struct Q8Cache {
   const uint8_t* kv8;
@@ -744,7 +759,8 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
     static_assert(2 * (sizeof(sgqa::QdSmem) + 512 + 1024) <= 233472, "two CTAs per SM");
     const size_t smem = sizeof(sgqa::QdSmem) + 512;
     auto kern = acc != nullptr ? sgqa::attn_q8_decode_kernel<true> : sgqa::attn_q8_decode_kernel<false>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done[2];
+    if ((s = allow_smem(kern, smem, done[acc != nullptr])) != SGQA_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * nsplit));
     cfg.blockDim = dim3(sgqa::kQdThreads);
@@ -780,7 +796,8 @@ sgqa_status do_attn_q8(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, 
   auto kern = skip_pairs ? sgqa::attn_q8_prefill_kernel<false, true> : sgqa::attn_q8_prefill_kernel<false, false>;
   for (int sweep = 0; sweep < (acc != nullptr ? 2 : 1); ++sweep) {
     if (sweep == 1) kern = sgqa::attn_q8_prefill_kernel<true, false>;
-    cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done[3];
+    if ((s = allow_smem(kern, smem, done[sweep == 1 ? 2 : skip_pairs])) != SGQA_OK) return s;
     kern<<<static_cast<unsigned>(units), sgqa::kQpThreads, smem, st>>>(
         m, static_cast<const __nv_bfloat16*>(q), c.scale, ids, msk, cnt, static_cast<const __nv_bfloat16*>(gate),
         static_cast<__nv_bfloat16*>(out), lse, acc, nq, p->num_kv_groups, p->topk, q0, c.blocks, scale_log2);
@@ -1253,7 +1270,8 @@ sgqa_status sgqa_evict(const sgqa_params* p, int64_t num_seqs, int64_t cache_cap
   if (n <= static_cast<int64_t>(sgqa::kEvMaxCluster) * sgqa::kEvSlots) {
     const size_t smem = sizeof(sgqa::EvictSmem);
     static_assert(sizeof(sgqa::EvictSmem) <= 232448, "select state exceeds shared memory");
-    cudaFuncSetAttribute(sgqa::evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done{0};
+    if ((s = allow_smem(sgqa::evict_select_kernel, smem, done)) != SGQA_OK) return s;
     cudaLaunchConfig_t cfg = {};
     const unsigned cl = static_cast<unsigned>(std::max<int64_t>(ncta, 1));
     cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * cl);

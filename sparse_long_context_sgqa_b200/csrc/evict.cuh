@@ -212,7 +212,8 @@ evict_select_long_kernel(const int64_t* acc, const int32_t* pos, int64_t known, 
 // counting; usually after two histograms.  Blocks with equal weights that reach
 // the last step are told apart by further histograms of their numbers.
 // Bound: latency (barriers and dependent passes), not bytes.
-// Measured: see evict_move_kernel.
+// Measured: 456 of 520 blocks kept 9.4 us, 16 x 4096 -> 2800 11.7 us, 2 x 65536 ->
+// 49152 28.6 us.
 // ---------------------------------------------------------------------------
 constexpr int kEvBins = 2048;
 constexpr int kEvSlots = 16384;      // per CTA
@@ -570,6 +571,9 @@ __device__ __forceinline__ void move_step(T* base, int words, int64_t step, cons
   }
 }
 
+// Moves of the kept blocks into the freed slots, array by array.
+// Bound: HBM.  Measured with the selection, in a CUDA graph: 16 x 4096 -> 2800 blocks
+// 76.9 us and 2 x 65536 -> 49152 132.7 us (bytes at the copy rate: 53.7, 93.1 us).
 __global__ void __launch_bounds__(kMoveWarps * 32, 4)
 evict_move_kernel(const __grid_constant__ EvictArrays ar, int arrays, int tail_arrays, EvictWs ws, int64_t n, int part, int64_t keep, int64_t slots) {
   const int64_t seq = blockIdx.y;

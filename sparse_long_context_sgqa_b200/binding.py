@@ -225,12 +225,12 @@ def alloc_workspace_q8(p: Params, num_seqs: int, nq: int, max_ctx: int, device) 
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
-def _check(name, t, dtype, numel):
-    """Address of a contiguous CUDA tensor of the values the call reads or writes there."""
-    if t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous():
+def _check(name, t, dtype, numel, dev):
+    """Address of a contiguous tensor of the values the call reads or writes there, on CUDA device `dev`."""
+    if t.dtype is dtype and t.numel() == numel and t.is_cuda and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {numel} {dtype} values, got {tuple(t.shape)} "
-                     f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    raise ValueError(f"{name}: expected a contiguous CUDA tensor of {numel} {dtype} values on the other tensors' device, "
+                     f"got {tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 # the current stream's handle without an object around it, where torch has that (a few microseconds per call)
@@ -254,39 +254,39 @@ def _run(fn, lead, stream, *args):
             _ok(fn(*args, raw))
 
 
-def _q8_cache(p, S, cap, kv8, kv_scale):
+def _q8_cache(p, S, cap, kv8, kv_scale, dev):
     n = S * cap // 8 * p.num_kv_groups * 2
-    return _check("kv8", kv8, torch.uint8, n * 8 * p.head_dim), _check("kv_scale", kv_scale, torch.float32, n)
+    return _check("kv8", kv8, torch.uint8, n * 8 * p.head_dim, dev), _check("kv_scale", kv_scale, torch.float32, n, dev)
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     if ws is None:
         return None, 0
     n = ws.numel()
-    return _check("workspace", ws, torch.uint8, n), n
+    return _check("workspace", ws, torch.uint8, n, dev), n
 
 
 def sgqa_kv_append_q8(p: Params, num_seqs, cache_cap, pos0, n, k, v, tail, kv8, kv_scale, stream=None):
     """Quantise the K/V rows of positions [pos0, pos0 + n) (k, v: [S, n, G, D] bf16) into the 8-bit cache."""
-    row = num_seqs * p.num_kv_groups * p.head_dim
+    row, dev = num_seqs * p.num_kv_groups * p.head_dim, kv8.get_device()
     _run(_lib.sgqa_kv_append_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, cache_cap, pos0, n,
-         _check("k", k, torch.bfloat16, row * n), _check("v", v, torch.bfloat16, row * n),
-         None if tail is None else _check("tail", tail, torch.bfloat16, row * 16),
-         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale))
+         _check("k", k, torch.bfloat16, row * n, dev), _check("v", v, torch.bfloat16, row * n, dev),
+         None if tail is None else _check("tail", tail, torch.bfloat16, row * 16, dev),
+         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale, dev))
 
 
 def sgqa_sparse_attn_q8(p: Params, num_seqs, q_pos0, nq, q, cache_cap, cache_len, kv8, kv_scale, sel, sel_count, out,
                         workspace=None, gate=None, acc=None, stream=None):
     """Attention over the 8-bit cache; acc ([S, cache_cap / 8] int64, units of 2^-32) gains the blocks' weights."""
     rows = num_seqs * nq * p.num_kv_groups
-    heads = rows * p.heads_per_group
+    heads, dev = rows * p.heads_per_group, kv8.get_device()
     _run(_lib.sgqa_sparse_attn_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, q_pos0, nq,
-         _check("q", q, torch.bfloat16, heads * p.head_dim), cache_cap, cache_len,
-         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale), _check("sel", sel, torch.int32, rows * p.topk),
-         _check("sel_count", sel_count, torch.int32, rows),
-         None if gate is None else _check("gate", gate, torch.bfloat16, heads),
-         None if acc is None else _check("acc", acc, torch.int64, num_seqs * cache_cap // 8),
-         _check("out", out, torch.bfloat16, heads * p.head_dim), *_workspace(workspace))
+         _check("q", q, torch.bfloat16, heads * p.head_dim, dev), cache_cap, cache_len,
+         *_q8_cache(p, num_seqs, cache_cap, kv8, kv_scale, dev), _check("sel", sel, torch.int32, rows * p.topk, dev),
+         _check("sel_count", sel_count, torch.int32, rows, dev),
+         None if gate is None else _check("gate", gate, torch.bfloat16, heads, dev),
+         None if acc is None else _check("acc", acc, torch.int64, num_seqs * cache_cap // 8, dev),
+         _check("out", out, torch.bfloat16, heads * p.head_dim, dev), *_workspace(workspace, dev))
 
 
 def sgqa_forward_q8(p: Params, num_seqs, q_pos0, nq, q, idx_q, idx_w, cache_cap, proxy_k, comp_logits, k, v, tail, kv8,
@@ -295,21 +295,22 @@ def sgqa_forward_q8(p: Params, num_seqs, q_pos0, nq, q, idx_q, idx_w, cache_cap,
     rows = num_seqs * nq * p.num_kv_groups
     heads, blocks = rows * p.heads_per_group, num_seqs * cache_cap // 8
     in_dt = torch.float32 if p.merge_in_f32 else torch.bfloat16
-    kv, sc = _q8_cache(p, num_seqs, cache_cap, kv8, kv_scale)
+    dev = kv8.get_device()
+    kv, sc = _q8_cache(p, num_seqs, cache_cap, kv8, kv_scale, dev)
     _run(_lib.sgqa_forward_q8, kv8, stream, ctypes.byref(p.c()), num_seqs, q_pos0, nq,
-         _check("q", q, torch.bfloat16, heads * p.head_dim),
-         _check("idx_q", idx_q, torch.bfloat16, rows * p.idx_heads * p.idx_dim),
-         _check("idx_w", idx_w, torch.float32, rows * p.idx_heads), cache_cap,
-         _check("proxy_k", proxy_k, in_dt, num_seqs * cache_cap * p.idx_dim),
-         _check("comp_logits", comp_logits, in_dt, num_seqs * cache_cap * p.idx_dim),
-         _check("k", k, torch.bfloat16, rows * p.head_dim), _check("v", v, torch.bfloat16, rows * p.head_dim),
-         None if tail is None else _check("tail", tail, torch.bfloat16, num_seqs * 16 * p.num_kv_groups * p.head_dim),
-         kv, sc, None if merged_f32 is None else _check("merged_f32", merged_f32, torch.float32, blocks * p.idx_dim),
-         _check("store", store, torch.uint8, blocks * p.idx_dim), _check("sel", sel, torch.int32, rows * p.topk),
-         _check("sel_count", sel_count, torch.int32, rows),
-         None if gate is None else _check("gate", gate, torch.bfloat16, heads),
-         None if acc is None else _check("acc", acc, torch.int64, blocks),
-         _check("out", out, torch.bfloat16, heads * p.head_dim), *_workspace(workspace))
+         _check("q", q, torch.bfloat16, heads * p.head_dim, dev),
+         _check("idx_q", idx_q, torch.bfloat16, rows * p.idx_heads * p.idx_dim, dev),
+         _check("idx_w", idx_w, torch.float32, rows * p.idx_heads, dev), cache_cap,
+         _check("proxy_k", proxy_k, in_dt, num_seqs * cache_cap * p.idx_dim, dev),
+         _check("comp_logits", comp_logits, in_dt, num_seqs * cache_cap * p.idx_dim, dev),
+         _check("k", k, torch.bfloat16, rows * p.head_dim, dev), _check("v", v, torch.bfloat16, rows * p.head_dim, dev),
+         None if tail is None else _check("tail", tail, torch.bfloat16, num_seqs * 16 * p.num_kv_groups * p.head_dim, dev),
+         kv, sc, None if merged_f32 is None else _check("merged_f32", merged_f32, torch.float32, blocks * p.idx_dim, dev),
+         _check("store", store, torch.uint8, blocks * p.idx_dim, dev), _check("sel", sel, torch.int32, rows * p.topk, dev),
+         _check("sel_count", sel_count, torch.int32, rows, dev),
+         None if gate is None else _check("gate", gate, torch.bfloat16, heads, dev),
+         None if acc is None else _check("acc", acc, torch.int64, blocks, dev),
+         _check("out", out, torch.bfloat16, heads * p.head_dim, dev), *_workspace(workspace, dev))
 
 
 def sgqa_evict_workspace_size(p: Params, num_seqs: int, cache_cap: int) -> int:
@@ -327,17 +328,18 @@ def sgqa_evict(p: Params, num_seqs, cache_cap, cache_len, keep, first, recent, a
     """Keep the `keep` heaviest blocks of every sequence.  arrays: contiguous tensors whose leading dimensions are
     (sequence, block) or (sequence, token); tail_arrays: the same, of which only the incomplete block moves."""
     blocks = num_seqs * (cache_cap // p.block_size)
-    n = len(arrays) + len(tail_arrays)
+    n, dev = len(arrays) + len(tail_arrays), acc.get_device()
     c = (_CacheArray * max(1, n))()
     for i, t in enumerate((*arrays, *tail_arrays) if tail_arrays else arrays):
         size = t.nbytes
-        if not t.is_cuda or not t.is_contiguous() or blocks == 0 or size % blocks:
-            raise ValueError("evict: every array is a contiguous CUDA tensor of cache_cap / block_size blocks per sequence")
+        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous() or blocks == 0 or size % blocks:
+            raise ValueError("evict: every array is a contiguous tensor of cache_cap / block_size blocks per sequence on acc's "
+                             "CUDA device")
         c[i] = (t.data_ptr(), size // blocks, i >= len(arrays))
     _run(_lib.sgqa_evict, acc, stream, ctypes.byref(p.c()), num_seqs, cache_cap, cache_len, keep, first, recent,
-         _check("acc", acc, torch.int64, blocks), None if pos is None else _check("pos", pos, torch.int32, blocks),
-         pos_count, evicted, _check("acc_out", acc_out, torch.int64, blocks), _check("pos_out", pos_out, torch.int32, blocks),
-         c, n, *_workspace(workspace))
+         _check("acc", acc, torch.int64, blocks, dev), None if pos is None else _check("pos", pos, torch.int32, blocks, dev),
+         pos_count, evicted, _check("acc_out", acc_out, torch.int64, blocks, dev), _check("pos_out", pos_out, torch.int32, blocks, dev),
+         c, n, *_workspace(workspace, dev))
 
 
 def sgqa_set_wait_limit_ns(ns: int):

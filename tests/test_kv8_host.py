@@ -241,3 +241,25 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
     other.device = torch.device("cuda:0")
     with pytest.raises(ValueError):
         Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, stream=other, **_append_tensors())
+
+
+@pytest.mark.parametrize("name", ["k", "v", "tail", "kv_scale"])
+def test_tensors_of_a_call_share_a_device(monkeypatch, name):
+    monkeypatch.setattr(Bd._lib, "sgqa_kv_append_q8", lambda *a: pytest.fail("called"))
+    t = _append_tensors()
+    t[name].device = torch.device("cuda:0")
+    with pytest.raises(ValueError, match=name):
+        Bd.sgqa_kv_append_q8(Params(), 2, 64, 0, 3, **t)
+
+
+@pytest.mark.parametrize("which", ["arrays", "tail_arrays", "pos_out", "workspace"])
+def test_evicted_arrays_share_a_device(monkeypatch, which):
+    monkeypatch.setattr(Bd._lib, "sgqa_evict", lambda *a: pytest.fail("called"))
+    t = {n: _Tensor((2, 8), torch.int32 if n.startswith("pos") else torch.int64) for n in ("acc", "pos", "acc_out", "pos_out")}
+    one, tail, ws = _Tensor((2, 8, 16), torch.uint8), _Tensor((2, 64, 4), torch.uint8), _Tensor((4096,), torch.uint8)
+    for x in (one, tail):
+        x.nbytes = x.numel()
+    {"arrays": one, "tail_arrays": tail, "pos_out": t["pos_out"], "workspace": ws}[which].device = torch.device("cuda:0")
+    with pytest.raises(ValueError):
+        Bd.sgqa_evict(Params(), 2, 64, 40, 2, 0, 0, t["acc"], t["pos"], 0, 0, t["acc_out"], t["pos_out"], [one], ws,
+                      tail_arrays=[tail])

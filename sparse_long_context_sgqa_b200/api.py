@@ -97,11 +97,13 @@ class SparseGQA:
         """Keep `keep` of the complete blocks of cache_len tokens; returns the new cache length.
 
         The blocks with the largest accumulated weight stay (acc: [S, capacity / B]
-        int64, by default the weights tracked with the 8-bit cache), and in any
+        int64, rearranged in place; where weights are tracked it is those), and in any
         case the `first` first and `recent` last blocks of the sequence.  The
         next call's q_pos0 is the returned length.
         """
         B = self.p.block_size
+        if acc is not None and self.acc is not None and acc is not self.acc:
+            raise ValueError("evict goes by the tracked weights here: with others those would keep the blocks' old slots")
         acc = self.acc if acc is None else acc
         if acc is None:
             raise ValueError("evict needs accumulated weights: track_weights or acc=")

@@ -263,3 +263,12 @@ def test_evicted_arrays_share_a_device(monkeypatch, which):
     with pytest.raises(ValueError):
         Bd.sgqa_evict(Params(), 2, 64, 40, 2, 0, 0, t["acc"], t["pos"], 0, 0, t["acc_out"], t["pos_out"], [one], ws,
                       tail_arrays=[tail])
+
+
+def test_evict_takes_the_tracked_weights_only(monkeypatch):
+    # with others the tracked ones would keep the blocks' old slots, and a later eviction would go by them
+    monkeypatch.setattr(Bd, "sgqa_evict", lambda *a, **kw: pytest.fail("called"))
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 64, 8, "cpu", kv_dtype="e4m3", track_weights=True)
+    with pytest.raises(ValueError):
+        m.evict(64, 4, acc=torch.ones((1, 8), dtype=torch.int64))
+    assert (m.evicted, m.pos_count) == (0, 0)

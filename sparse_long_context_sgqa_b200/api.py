@@ -14,6 +14,8 @@ accumulates each block's attention weight in ``acc`` along the way.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as Bd
@@ -108,8 +110,10 @@ class SparseGQA:
         if acc is None:
             raise ValueError("evict needs accumulated weights: track_weights or acc=")
         if self.pos is None:
-            self.pos = torch.empty((self.S, self.cap // B), dtype=torch.int32, device=self.device)
-            self._evict_ws = Bd.alloc_evict_workspace(self.p, self.S, self.cap, self.device)
+            # on the call's stream: memory that another stream's work still uses is not handed to it
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                self._evict_ws = Bd.alloc_evict_workspace(self.p, self.S, self.cap, self.device)
+                self.pos = torch.empty((self.S, self.cap // B), dtype=torch.int32, device=self.device)
         kv = [self.kv8, self.kv_scale] if self.kv_dtype == "e4m3" else [self.k, self.v]
         arrays = kv + [self.store] + ([self.merged] if self.merged is not None else [])
         n = cache_len // B

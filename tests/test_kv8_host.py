@@ -272,3 +272,23 @@ def test_evict_takes_the_tracked_weights_only(monkeypatch):
     with pytest.raises(ValueError):
         m.evict(64, 4, acc=torch.ones((1, 8), dtype=torch.int64))
     assert (m.evicted, m.pos_count) == (0, 0)
+
+
+def test_evict_allocates_on_the_calls_stream(monkeypatch):
+    class On:
+        def __init__(self, st):
+            self.st = st
+
+        def __enter__(self):
+            cur.append(self.st)
+
+        def __exit__(self, *a):
+            cur.pop()
+
+    cur, seen = [], []
+    monkeypatch.setattr(api.torch.cuda, "stream", On)
+    monkeypatch.setattr(Bd, "alloc_evict_workspace", lambda *a: seen.append(list(cur)) or "ws")
+    monkeypatch.setattr(Bd, "sgqa_evict", lambda *a, **kw: seen.append(kw["stream"]))
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 64, 8, "cpu", kv_dtype="e4m3", track_weights=True)
+    m.evict(64, 4, stream="side")
+    assert seen == [["side"], "side"]

@@ -149,7 +149,7 @@ class SparseGQA:
                 (S, n, G), dtype=torch.int32, device=self.device)
             o = out[:, c0:c0 + n] if S == 1 else torch.empty((S, n) + tuple(out.shape[2:]),
                                                              dtype=out.dtype, device=self.device)
-            rows = {} if k is None and v is None else {"k": k[:, c0:c0 + n].contiguous(), "v": v[:, c0:c0 + n].contiguous()}
+            rows = {x: t[:, c0:c0 + n].contiguous() for x, t in (("k", k), ("v", v)) if t is not None}
             self.forward(q_pos0 + c0, q[:, c0:c0 + n].contiguous(), idx_q[:, c0:c0 + n].contiguous(),
                          idx_w[:, c0:c0 + n].contiguous(), s_sel, s_cnt, o, stream=stream,
                          gate=None if gate is None else gate[:, c0:c0 + n].contiguous(), **rows)

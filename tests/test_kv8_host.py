@@ -292,3 +292,13 @@ def test_evict_allocates_on_the_calls_stream(monkeypatch):
     m = api.SparseGQA(Params(num_kv_groups=1), 1, 64, 8, "cpu", kv_dtype="e4m3", track_weights=True)
     m.evict(64, 4, stream="side")
     assert seen == [["side"], "side"]
+
+
+@pytest.mark.parametrize("missing", ["k", "v"])
+def test_prefill_refuses_half_of_the_rows(monkeypatch, missing):
+    monkeypatch.setattr(Bd, "sgqa_forward_q8", lambda *a, **kw: pytest.fail("called"))
+    m = api.SparseGQA(Params(num_kv_groups=1, topk=4), 1, 64, 8, "cpu", kv_dtype="e4m3")
+    q = torch.zeros((1, 4, 16, 192), dtype=torch.bfloat16)
+    rows = {n: torch.zeros((1, 4, 1, 192), dtype=torch.bfloat16) for n in ("k", "v") if n != missing}
+    with pytest.raises(ValueError, match="K/V rows"):
+        m.prefill(q, torch.zeros((1, 4, 1, 8, 128)), torch.zeros((1, 4, 1, 8)), torch.empty_like(q), **rows)

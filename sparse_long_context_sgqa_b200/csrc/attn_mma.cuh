@@ -209,7 +209,11 @@ attn_plan_sort_kernel(const int32_t* __restrict__ sel, const int32_t* __restrict
     plan_mask[obase + pos] = static_cast<uint8_t>(m);
     ++pos;
   }
-  if (tid == kPlanSortThreads - 1) plan_count[unit] = pos;
+  if (tid == kPlanSortThreads - 1) {
+    plan_count[unit] = pos;
+    // consumers read the masks eight at a time: zeros behind the last one, as above
+    for (; (pos & 7) != 0; ++pos) plan_mask[obase + pos] = 0;
+  }
 }
 
 // ---------------------------------------------------------------------------

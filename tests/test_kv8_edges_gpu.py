@@ -1,0 +1,58 @@
+"""The 8-bit cache's operators at their edges: wide contexts, scores that underflow, calls that gave up, lists out of order,
+other scales, sinks.  Tolerances: tests/_kv8_ref.py and tests/test_kv8_gpu.py, unless a test derives its own.
+"""
+
+import pytest
+import torch
+
+from sparse_long_context_sgqa_b200.binding import Params
+from tests import _kv8_ref as R
+from tests import test_kv8_gpu as T
+
+pytestmark = pytest.mark.gpu
+D, HG, B = R.D, R.HG, R.B
+
+
+@pytest.fixture(scope="module")
+def Bd():
+    from sparse_long_context_sgqa_b200 import binding
+    return binding
+
+
+# ------------------ wide id ranges
+@pytest.mark.parametrize("weights", [False, True])
+def test_union_of_a_context_too_wide_for_a_bitmap(Bd, cuda_device, weights):
+    # 11.8 M tokens: a unit's union is planned by sorting.  Short lists, so that unions end inside a tile, and a workspace
+    # of ones, which an earlier call may well leave there.
+    H, nq, k, dev = 1_480_000, 40, 24, cuda_device
+    q0, blocks, g = 8 * H + 3, H + 7, T.gen(11)
+    used = torch.cat([torch.tensor([0, H - 1]), torch.randperm(H - 2, generator=g)[:58] + 1]).sort().values.unique()
+    n = len(used)
+    idx = torch.cat([used, torch.arange(H, blocks)])
+    codes = (torch.randn((len(idx), 1, 2, B, D), generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    small_sc = torch.exp2(torch.randint(-9, -6, (len(idx), 1, 2), generator=g).float())
+    kv8 = torch.empty((1, blocks, 1, 2, B, D), dtype=torch.uint8, device=dev)
+    sc = torch.ones((1, blocks, 1, 2), device=dev)
+    kv8[0, idx.to(dev)], sc[0, idx.to(dev)] = codes.to(dev), small_sc.to(dev)
+    q = torch.randn((1, nq, HG, D), generator=g).to(torch.bfloat16)
+    sel = torch.full((1, nq, 1, k), -1, dtype=torch.int32)
+    cnt = torch.zeros((1, nq, 1), dtype=torch.int32)
+    small_sel = sel.clone()
+    for i in range(nq):
+        c = int(torch.randint(0, 6, (1,), generator=g))
+        pick = torch.randperm(n, generator=g)[:c].sort().values
+        sel[0, i, 0, :c], small_sel[0, i, 0, :c], cnt[0, i, 0] = used[pick].int(), pick.int(), c
+    p = Params(num_kv_groups=1, topk=k)
+    ws = Bd.alloc_workspace_q8(p, 1, nq, q0 + nq, dev)
+    ws.fill_(255)
+    out = torch.zeros_like(q, device=dev)
+    acc = torch.zeros((1, blocks), dtype=torch.int64, device=dev) if weights else None
+    Bd.sgqa_sparse_attn_q8(p, 1, q0, nq, q.to(dev), 8 * blocks, q0 + nq, kv8, sc, sel.to(dev), cnt.to(dev), out, ws, acc=acc)
+    Bd.sgqa_check()
+    # the reference over the blocks that occur, renumbered in order
+    ref, tol, wts = R.attention(q.double().numpy(), R.codes_to_values(codes)[None], small_sc.double().numpy()[None],
+                                small_sel.numpy(), cnt.numpy(), 8 * n + 3)
+    R.check_out(out, ref, tol)
+    if weights:
+        T.check_weights(acc[:, idx.to(dev)], 0, wts, 2 * nq)
+        assert int(acc.sum()) == int(acc[:, idx.to(dev)].sum())

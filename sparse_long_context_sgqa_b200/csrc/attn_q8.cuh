@@ -991,11 +991,18 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       tc::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
       tc::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
       tc::tmem_ld_wait();
-      if (last) {  // tokens of the row's current block behind t
+      float rct = rc;  // this tile's row scale
+      if (last) {
+        // Tokens of the row's current block behind t get score -inf.  Where the row's
+        // and the block's scale underflow together (a head of zeros at keys of
+        // zeros), -inf times their product would be NaN: the scores are 0 then, and
+        // stay apart from the masked ones under a row scale of 1.
         const int end = static_cast<int>(t - c0);
+        const bool flat = meta[use[0] >> 8 ? 1 : 0].x * rc == 0.f;
+        if (flat) rct = 1.f;
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          if (x > end && ((use[0] >> (8 * (x >> 3))) & 1u)) sr[x] = __float_as_uint(-INFINITY);
+          if ((use[0] >> (8 * (x >> 3))) & 1u) sr[x] = x > end ? __float_as_uint(-INFINITY) : flat ? 0u : sr[x];
       }
       if constexpr (WEIGHTS) {
         tc::fence_before();
@@ -1005,7 +1012,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float cf = meta[e].x * rc;
+          const float cf = meta[e].x * rct;
           const uint64_t c2 = pack_f32x2(cf, cf), o2 = pack_f32x2(-row_lse, -row_lse);
           uint64_t p[4];
 #pragma unroll
@@ -1059,7 +1066,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
                 for (int e = e2; e < e2 + 2; ++e) {
                   // P = 2^(s + log2 vs - ref); a block the row does not attend has offset -inf
                   const float4 mt = meta[4 * h + e];
-                  const float cf = mt.x * rc, off = (use[h] >> (8 * e)) & 1u ? mt.y + neg : -INFINITY;
+                  const float cf = mt.x * rct, off = (use[h] >> (8 * e)) & 1u ? mt.y + neg : -INFINITY;
                   const uint64_t c2 = pack_f32x2(cf, cf), o2 = pack_f32x2(off, off);
                   uint64_t pe[4];
 #pragma unroll
@@ -1094,7 +1101,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
             float v = __uint_as_float(sr[8 * e]);
 #pragma unroll
             for (int x = 1; x < 8; ++x) v = fmaxf(v, __uint_as_float(sr[8 * e + x]));
-            mx = fmaxf(mx, (use[e >> 2] >> (8 * (e & 3))) & 1u ? fmaf(v, mt.x * rc, mt.y) : -INFINITY);
+            mx = fmaxf(mx, (use[e >> 2] >> (8 * (e & 3))) & 1u ? fmaf(v, mt.x * rct, mt.y) : -INFINITY);
           }
           // A new reference lies 4 below the largest weight: FP16 then holds weights
           // down to 2^-18 of it in full and resolves 2^-28 of it, and the reference

@@ -56,3 +56,21 @@ def test_union_of_a_context_too_wide_for_a_bitmap(Bd, cuda_device, weights):
     if weights:
         T.check_weights(acc[:, idx.to(dev)], 0, wts, 2 * nq)
         assert int(acc.sum()) == int(acc[:, idx.to(dev)].sum())
+
+
+# ------------------ scores that underflow
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -60])
+def test_zero_heads_against_zero_keys(Bd, cuda_device, nq, size):
+    # a head of zeros (or far below the others) at a current block of zero keys, as padding leaves them: the product of
+    # both scales is below FP32's range, every score is 0, and the tokens behind the query stay out
+    c = T.make_attn(2, 2, nq, 1002, 50, cuda_device)
+    c["q"][:, :, 3:7] = size
+    c["q"][:, :, 19] = -size
+    first, last = 1002 // B, (1002 + nq - 1) // B
+    c["kv8"][:, first:last + 1, :, 0] = 0
+    c["sc"][:, first:last + 1, :, 0] = 2.0 ** -100
+    ref, tol, weights = T.reference(c)
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    T.check_attn(c, T.run_attn(Bd, c, acc=acc), ref, tol)
+    T.check_weights(acc, 0, weights, nq * 2 * 2)

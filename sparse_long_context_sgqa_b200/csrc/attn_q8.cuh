@@ -521,9 +521,12 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
       for (int x = threadIdx.x - 64; x < kHg * kQdOStride; x += 256) (&po.o[0][0])[x] = 0.f;
     }
     if (lane == 0) {
+      // a split that gave up has no sums: NaN makes the whole row NaN and keeps its
+      // weights out of acc, which outlives the call
+      const bool gave_up = sm.abort != 0;
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
-        po.wl[quad][h0 + h] = l[h];
+        po.wl[quad][h0 + h] = gave_up ? __uint_as_float(0x7FC00000u) : l[h];
         if (quad == 0) po.m[h0 + h] = ref[h];
       }
     }

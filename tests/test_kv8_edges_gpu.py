@@ -74,3 +74,34 @@ def test_zero_heads_against_zero_keys(Bd, cuda_device, nq, size):
     acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
     T.check_attn(c, T.run_attn(Bd, c, acc=acc), ref, tol)
     T.check_weights(acc, 0, weights, nq * 2 * 2)
+
+
+# ------------------ calls that gave up
+def gave_up(Bd, cuda_device, nq, limits):
+    c = T.make_attn(2, 4, nq, 3000, 256, cuda_device)
+    p = Params(num_kv_groups=4, topk=256)
+    ws = Bd.alloc_workspace_q8(p, 2, nq, 3000 + nq, cuda_device)
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    T.run_attn(Bd, c, acc=acc, ws=ws)
+    once, failed = acc.clone(), 0
+    for ns in limits:
+        ws.zero_()  # (stale sums and log-sums of 0 would count as large weights)
+        before = acc.clone()
+        try:
+            Bd.sgqa_set_wait_limit_ns(ns)
+            T.run_attn(Bd, c, acc=acc, ws=ws)
+        except Bd.SgqaError as e:
+            assert e.code == 5
+            failed += 1
+        finally:
+            Bd.sgqa_set_wait_limit_ns(0)
+        added = acc - before
+        assert (added >= 0).all() and (added <= once).all(), (ns, int(added.min()), int((added - once).max()))
+    assert failed >= 1
+    before = acc.clone()
+    T.run_attn(Bd, c, acc=acc, ws=ws)
+    assert torch.equal(acc - before, once)
+
+
+def test_few_queries_that_gave_up_add_no_weights_of_their_own(Bd, cuda_device):
+    gave_up(Bd, cuda_device, 1, [1, 1, 500, 1000, 2000, 4000, 5000, 6000, 7000, 8000, 10000])

@@ -297,6 +297,8 @@ sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t ca
  *        every block in units of 2^-32: the call adds the softmax weights (before
  *        the gate) that its queries' heads, of all groups, give to the block's
  *        tokens.  Integer sums: their order does not matter.  NaN weights add 0.
+ *        Of a call that sgqa_check reports as SGQA_ERR_TIMEOUT a part of the
+ *        weights, possibly none, has been added.
  * sel ids must be strictly ascending and below floor(t/8); others are left out
  * and reported by sgqa_check as SGQA_ERR_DEVICE.
  * kv_scale: as sgqa_kv_append_q8 writes it: positive (or NaN), at least 2^-100.

@@ -1036,8 +1036,9 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
         float v = (h1 ? z[1] : z[0]) + __shfl_xor_sync(0xffffffffu, h1 ? z[0] : z[1], 1);
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
-        // (after a wait that gave up the block numbers may never have been written)
-        if (ok && lane < 8 && v > 0.f) {
+        // After a wait that gave up, anywhere in the unit, scores may be overwritten
+        // early and block numbers never written: nothing more is added.
+        if (ok && !*abort && lane < 8 && v > 0.f) {
           const int64_t id = last ? cb + lane : sm.ids[slot][at + lane];
           if (id >= 0 && id < blocks) acc_add(acc + seq * blocks + id, v);
         }
@@ -1188,6 +1189,11 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
       if (tc::elect_one()) tc::mma_commit(bar(d));
       __syncwarp();
       tc::mbar_drain(bar(d), 0);
+    } else if (!WEIGHTS && lse != nullptr && warp >= 12) {
+      // no log-sums: the weights' sweep, which may well succeed, adds nothing for these rows
+      const int m = threadIdx.x - 384;
+      const int64_t qi = qb * 8 + (m >> 4);
+      if (qi < nq) lse[((seq * nq + qi) * G + g) * kHg + (m & 15)] = __uint_as_float(0x7FC00000u);
     }
   }
   tc::fence_before();

@@ -105,3 +105,8 @@ def gave_up(Bd, cuda_device, nq, limits):
 
 def test_few_queries_that_gave_up_add_no_weights_of_their_own(Bd, cuda_device):
     gave_up(Bd, cuda_device, 1, [1, 1, 500, 1000, 2000, 4000, 5000, 6000, 7000, 8000, 10000])
+
+
+# ------------------ calls that gave up, many queries
+def test_many_queries_that_gave_up_add_no_weights_of_their_own(Bd, cuda_device):
+    gave_up(Bd, cuda_device, 64, [1, 1, 500, 1000, 2000, 4000, 5000, 6000, 7000, 8000, 10000])

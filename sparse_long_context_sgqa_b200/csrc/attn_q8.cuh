@@ -1098,6 +1098,7 @@ attn_q8_prefill_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bfl
           // weights is above 2^12 then), or the row has no reference yet
           const bool high = top > 60000.f || (ref == -INFINITY && (use[0] | use[1]) != 0u);
           if (!__any_sync(0xffffffffu, high)) break;
+          tc::tmem_st_wait();  // the second pass stores to the same columns: stores keep no order of their own
           float mx = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {

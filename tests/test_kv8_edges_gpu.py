@@ -1,7 +1,9 @@
 """The 8-bit cache's operators at their edges: wide contexts, scores that underflow, calls that gave up, lists out of order,
 other scales, sinks.  Tolerances: tests/_kv8_ref.py and tests/test_kv8_gpu.py, unless a test derives its own.
 """
+import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -110,3 +112,30 @@ def test_few_queries_that_gave_up_add_no_weights_of_their_own(Bd, cuda_device):
 # ------------------ calls that gave up, many queries
 def test_many_queries_that_gave_up_add_no_weights_of_their_own(Bd, cuda_device):
     gave_up(Bd, cuda_device, 64, [1, 1, 500, 1000, 2000, 4000, 5000, 6000, 7000, 8000, 10000])
+
+
+# ------------------ a reference that moves in every tile
+@pytest.mark.parametrize("nq", [1, 70])
+def test_scores_that_grow_along_the_list(Bd, cuda_device, nq):
+    # the first coordinate climbs by about 2^14 of weight per eight selected blocks: every tile's weights are computed twice
+    c = T.make_attn(1, 2, nq, 6000, 200, cuda_device, sigma=0.3, spread=0)
+    blocks = c["cap"] // B
+    c["q"][..., 0] = 8.0
+    c["kv8"][:, :, :, 0, :, 0] = torch.tensor(448.0).to(torch.float8_e4m3fn).view(torch.uint8).to(cuda_device)
+    step = 14 * math.log(2) * math.sqrt(D) / (8 * 448) * 200 / (8 * 750)
+    c["sc"][:, :, :, 0] = (1 + torch.arange(blocks, device=cuda_device))[None, :, None] * step
+    ref, tol, weights = T.reference(c)
+    outs = []
+    for _ in range(6):
+        acc = torch.zeros((1, blocks), dtype=torch.int64, device=cuda_device)
+        outs.append((T.run_attn(Bd, c, acc=acc), acc))
+    T.check_attn(c, outs[0][0], ref, tol)
+    # Weights at scores of up to 480 (powers of two): a query value other than the row's largest, 8, is off by up to
+    # 2^-17.8 of that (few queries: 2^-21.8), a score by that times its key; FP32 adds 2^-15 at magnitude 30, so 2^-11.
+    # A weight takes a score's error and its row's sum the largest of them: twice.
+    keys = (R.codes_to_values(c["kv8"])[0, :, :, 0, :, 1:] * c["sc"][0, :, :, 0].cpu().double().numpy()[:, :, None, None])
+    far = 8 * 2.0 ** (-21.8 if nq <= 32 else -17.8) * np.abs(keys).sum(-1).max() / math.sqrt(D)
+    rel = math.expm1(2 * (far + 2.0 ** -11 * math.log(2)))
+    off = np.abs(outs[0][1].cpu().double().numpy() * R.UNIT - weights)
+    assert rel < 0.1 and (off <= rel * weights + nq * 2 * 2 * R.UNIT).all()
+    assert all(torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16)) and torch.equal(a, outs[0][1]) for o, a in outs)

@@ -53,7 +53,18 @@ std::atomic<uint64_t> g_launches{0};
     g_launches.fetch_add(1, std::memory_order_relaxed);   \
   } while (0)
 
+// The dynamic shared memory a kernel may use.  The limit holds for the whole
+// process: where a call's size depends on its arguments `bytes` is the largest
+// that any call takes, or one host thread could lower it under another's launch.
+template <typename K>
+sgqa_status set_smem(K kern, size_t bytes) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  return e == cudaSuccess ? SGQA_OK : cuda_fail(e, "cudaFuncSetAttribute(shared memory)");
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int kMaxTopk = 2048;
 
 sgqa_status check_params(const sgqa_params* p) {
   if (p == nullptr) return fail(SGQA_ERR_INVALID_ARGUMENT, "params is NULL");
@@ -66,7 +77,7 @@ sgqa_status check_params(const sgqa_params* p) {
     return fail(SGQA_ERR_UNSUPPORTED, "idx_heads must be 4 or 8");
   const int B = p->block_size;
   if (B != 1 && B != 2 && B != 4 && B != 8) return fail(SGQA_ERR_UNSUPPORTED, "block_size must be 1, 2, 4 or 8");
-  if (p->topk > 2048) return fail(SGQA_ERR_UNSUPPORTED, "topk must be <= 2048");
+  if (p->topk > kMaxTopk) return fail(SGQA_ERR_UNSUPPORTED, "topk must be <= %d", kMaxTopk);
   if (p->merge_in_f32 != 0 && p->merge_in_f32 != 1)
     return fail(SGQA_ERR_INVALID_ARGUMENT, "merge_in_f32 must be 0 or 1");
   return SGQA_OK;
@@ -418,8 +429,9 @@ sgqa_status do_index(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, co
       if (p->topk <= 512) {
         const int nwords_max = static_cast<int>((rneed + 31) / 32);
         const size_t dsmem = static_cast<size_t>(2 * sgqa::kFilterCap + nwords_max) * 4;
-        if (dsmem > 227 * 1024) return fail(SGQA_ERR_UNSUPPORTED, "context too long for the staged top-k kernel");
-        cudaFuncSetAttribute(sgqa::topk_staged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsmem);
+        constexpr size_t kMost = 232448 - 8304;  // beside the kernel's static shared memory
+        if (dsmem > kMost) return fail(SGQA_ERR_UNSUPPORTED, "context too long for the staged top-k kernel");
+        if ((s = set_smem(sgqa::topk_staged_kernel, kMost)) != SGQA_OK) return s;
         sgqa::topk_staged_kernel<<<static_cast<unsigned>(rows), sgqa::kStagedThreads, dsmem, st>>>(
             staging, staged, nq, G, q0, B, p->topk, w.f.subcap, nwords_max, sel, sel_count, flags, list, list_count);
         SGQA_LAUNCH_CHECK("topk_staged_kernel");
@@ -489,6 +501,7 @@ sgqa_status do_index(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, co
     return SGQA_OK;
   }
   const int nwords = static_cast<int>((std::max<int64_t>(rneed, 1) + 31) / 32);
+  constexpr size_t kRows2Most = 112 * 1024;
   const size_t ssmem = (static_cast<size_t>(sgqa::kRows2Warps) * sgqa::kRows2Bins / 2 + 2 * sgqa::kRows2Cand + nwords) * 4;
   // Rows of 2048 .. 16384 candidates: a sampled threshold, one pass over the
   // row keeping the survivors, a linear histogram and an exact boundary-bin
@@ -506,8 +519,9 @@ sgqa_status do_index(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, co
         scores, w.rpad, nq, G, q0, B, p->topk, sel, sel_count, list, list_count);
     SGQA_LAUNCH_CHECK("topk_rows_list_kernel");
     return SGQA_OK;
-  } else if (rneed >= 32768 && ssmem <= 112 * 1024) {
-    cudaFuncSetAttribute(sgqa::topk_rows2_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssmem);
+  } else if (rneed >= 32768 && ssmem <= kRows2Most) {
+    sgqa_status s = set_smem(sgqa::topk_rows2_kernel, kRows2Most);
+    if (s != SGQA_OK) return s;
     cudaError_t e = cudaMemsetAsync(list_count, 0, 4, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(list count)");
     sgqa::topk_rows2_kernel<<<static_cast<unsigned>(rows), sgqa::kRows2Threads, ssmem, st>>>(
@@ -539,15 +553,17 @@ sgqa_status launch_plan(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq,
   };
   const int pshift = plan_smem(0) <= 96 * 1024 ? 0 : 3;
   const size_t psmem = plan_smem(pshift);
-  if (psmem <= 200 * 1024) {
-    cudaFuncSetAttribute(sgqa::attn_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)psmem);
+  constexpr size_t kMost = 200 * 1024;
+  sgqa_status s;
+  if (psmem <= kMost) {
+    if ((s = set_smem(sgqa::attn_plan_kernel, kMost)) != SGQA_OK) return s;
     sgqa::attn_plan_kernel<<<static_cast<unsigned>(units), sgqa::kPlanThreads, psmem, st>>>(
         sel, sel_count, nq, G, k, nwords, pshift, q0, B, ids, msk, cnt);
     SGQA_LAUNCH_CHECK("attn_plan_kernel");
   } else {
     const int pow2 = plan_pow2(k);
     const size_t ssmem = static_cast<size_t>(pow2) * 4;
-    cudaFuncSetAttribute(sgqa::attn_plan_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ssmem);
+    if ((s = set_smem(sgqa::attn_plan_sort_kernel, static_cast<size_t>(plan_pow2(kMaxTopk)) * 4)) != SGQA_OK) return s;
     sgqa::attn_plan_sort_kernel<<<static_cast<unsigned>(units), sgqa::kPlanSortThreads, ssmem, st>>>(
         sel, sel_count, nq, G, k, pow2, q0, B, ids, msk, cnt);
     SGQA_LAUNCH_CHECK("attn_plan_sort_kernel");
@@ -640,8 +656,7 @@ sgqa_status do_attn(const sgqa_params* p, int64_t S, int64_t q0, int64_t nq, con
   return do_attn_kv(p, S, q0, nq, q, kv, sel, sel_count, out, gate, ws, st);
 }
 
-// Dynamic shared memory a kernel may use, raised once per device and kernel
-// (`done`: a bit per device) rather than on every call.
+// The same once per device and kernel (`done`: a bit per device) rather than on every call.
 template <typename K>
 sgqa_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
@@ -649,8 +664,8 @@ sgqa_status allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return SGQA_OK;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared memory)");
+  sgqa_status s = set_smem(kern, bytes);
+  if (s != SGQA_OK) return s;
   done.fetch_or(bit, std::memory_order_release);
   return SGQA_OK;
 }

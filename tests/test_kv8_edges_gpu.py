@@ -1,7 +1,9 @@
 """The 8-bit cache's operators at their edges: wide contexts, scores that underflow, calls that gave up, lists out of order,
 other scales, sinks.  Tolerances: tests/_kv8_ref.py and tests/test_kv8_gpu.py, unless a test derives its own.
 """
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -139,3 +141,55 @@ def test_scores_that_grow_along_the_list(Bd, cuda_device, nq):
     off = np.abs(outs[0][1].cpu().double().numpy() * R.UNIT - weights)
     assert rel < 0.1 and (off <= rel * weights + nq * 2 * 2 * R.UNIT).all()
     assert all(torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16)) and torch.equal(a, outs[0][1]) for o, a in outs)
+
+
+# ------------------ calls of several host threads
+def test_threads_with_contexts_of_different_length(Bd, cuda_device):
+    # the planner's shared memory goes by the context; one thread's calls must not take it from another's
+    dev, g, nq, k = cuda_device, T.gen(4), 40, 8
+    jobs = []
+    for H in (300, 380_000):
+        q0, blocks = 8 * H, H + 6
+        kv8 = torch.zeros((1, blocks, 1, 2, B, D), dtype=torch.uint8, device=dev)
+        kv8[:, :300] = torch.randint(0, 127, (1, 300, 1, 2, B, D), generator=g, dtype=torch.uint8).to(dev)
+        sel = torch.stack([torch.randperm(300, generator=g)[:k].sort().values for _ in range(nq)]).view(1, nq, 1, k)
+        p = Params(num_kv_groups=1, topk=k)
+        jobs.append(dict(p=p, q0=q0, cap=8 * blocks, q=(torch.randn((1, nq, HG, D), generator=g) * 0.01).to(torch.bfloat16).to(dev),
+                         kv8=kv8, sc=torch.full((1, blocks, 1, 2), 2.0 ** -8, device=dev), sel=sel.int().to(dev),
+                         cnt=torch.full((1, nq, 1), k, dtype=torch.int32, device=dev),
+                         out=torch.zeros((1, nq, HG, D), dtype=torch.bfloat16, device=dev),
+                         ws=Bd.alloc_workspace_q8(p, 1, nq, q0 + nq, dev), stream=torch.cuda.Stream(device=dev)))
+
+    def call(j):  # the library's call itself: host threads are inside it at once more often
+        a = j.get("args")
+        if a is None:
+            ptr = {x: t.data_ptr() for x, t in j.items() if torch.is_tensor(t)}
+            a = j["args"] = (ctypes.byref(j["p"].c()), 1, j["q0"], nq, ptr["q"], j["cap"], j["q0"] + nq, ptr["kv8"], ptr["sc"],
+                             ptr["sel"], ptr["cnt"], None, None, ptr["out"], ptr["ws"], j["ws"].numel(), j["stream"].cuda_stream)
+        Bd._ok(Bd._lib.sgqa_sparse_attn_q8(*a))
+
+    want = []
+    torch.cuda.synchronize()
+    for j in jobs:
+        call(j)
+        torch.cuda.synchronize()
+        want.append(j["out"].clone())
+    errors = []
+
+    def work(j):
+        try:
+            torch.cuda.set_device(dev)
+            for _ in range(4000):
+                call(j)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    Bd.sgqa_check()
+    assert not errors, errors[0]
+    assert all(torch.equal(j["out"], w) for j, w in zip(jobs, want))

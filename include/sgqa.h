@@ -68,9 +68,10 @@ typedef struct {
 
 /*
  * Bytes of workspace a call with these sizes needs (for sgqa_index_topk,
- * sgqa_sparse_attn and sgqa_forward alike).  nq = queries per sequence per
- * call, max_ctx = the largest q_pos0 + nq the workspace will serve.  The
- * workspace must be 256-byte aligned.  Pure host computation; no CUDA call.
+ * sgqa_sparse_attn and sgqa_forward alike).  nq = the most queries per sequence
+ * of a call (calls of fewer are served too), max_ctx = the largest q_pos0 + nq
+ * the workspace will serve.  The workspace must be 256-byte aligned.  Pure host
+ * computation; no CUDA call.
  */
 sgqa_status sgqa_workspace_size(const sgqa_params* p, int64_t num_seqs, int64_t nq,
                                 int64_t max_ctx, size_t* bytes);

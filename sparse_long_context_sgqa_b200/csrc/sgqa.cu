@@ -893,9 +893,14 @@ sgqa_status sgqa_workspace_size(const sgqa_params* p, int64_t num_seqs, int64_t 
   if (s != SGQA_OK) return s;
   if (bytes == nullptr) return fail(SGQA_ERR_INVALID_ARGUMENT, "bytes is NULL");
   if (num_seqs < 1 || nq < 0 || max_ctx < nq) return fail(SGQA_ERR_INVALID_ARGUMENT, "bad sizes");
-  const size_t iw = index_ws_bytes_upto(p, num_seqs, nq, std::max<int64_t>(max_ctx, 1));
-  const AttnWs aw = attn_ws(p, num_seqs, nq);
-  *bytes = std::max(iw, aw.bytes);
+  // Calls of nq queries and, on the decode path, of any fewer: there a row of a
+  // smaller call has more splits, so fewer queries can need more.
+  const int64_t few = std::min(nq, kDecodeMaxNq);
+  max_ctx = std::max<int64_t>(max_ctx, 1);
+  size_t most = std::max({index_ws_bytes_upto(p, num_seqs, nq, max_ctx), index_ws_bytes_upto(p, num_seqs, few, max_ctx),
+                          attn_ws(p, num_seqs, nq).bytes});
+  for (int64_t n = 1; n <= few; ++n) most = std::max(most, attn_ws(p, num_seqs, n).bytes);
+  *bytes = most;
   return SGQA_OK;
 }
 

@@ -193,3 +193,52 @@ def test_threads_with_contexts_of_different_length(Bd, cuda_device):
     Bd.sgqa_check()
     assert not errors, errors[0]
     assert all(torch.equal(j["out"], w) for j, w in zip(jobs, want))
+
+
+# ------------------ a BF16 cache
+def test_evict_a_bf16_cache_by_given_weights(Bd, cuda_device):
+    from sparse_long_context_sgqa_b200.api import SparseGQA
+    dev, S, G, H, cap, n, part = cuda_device, 2, 2, 4, 512, 43, 3
+    p = Params(num_kv_groups=G, idx_heads=H, topk=9)
+    g = T.gen(6)
+    r = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).to(dev)  # noqa: E731
+    m = SparseGQA(p, S, cap, 16, dev, keep_merged_f32=True)
+    for t in (m.k, m.v, m.kp, m.c):
+        t.copy_(r(*t.shape))
+    Bd.sgqa_merge_blocks(p, S, cap, m.kp, m.c, 0, n, m.merged, m.store)
+    acc = torch.randint(0, 1 << 40, (S, cap // B), generator=g).to(dev)
+    length = n * B + part
+    before = {x: getattr(m, x).clone() for x in ("k", "v", "kp", "c", "store", "merged")}
+    acc0 = acc.cpu()
+    with pytest.raises(ValueError):
+        m.evict(length, 20)
+    new = m.evict(length, 20, first=2, recent=4, acc=acc)
+    Bd.sgqa_check()
+    assert new == 20 * B + part and (m.evicted, m.pos_count) == (23, 20)
+    other = SparseGQA(p, S, cap, 16, dev)
+    for s in range(S):
+        src, new_acc, num = R.evict(n, True, 20, 2, 4, acc0[s].tolist(), [], 0, 0)
+        assert np.array_equal(acc[s].cpu().numpy(), new_acc) and m.pos[s, :20].tolist() == num
+        rows = torch.cat([torch.arange(b * B, b * B + B) for b in src]).to(dev)
+        for x in ("k", "v"):
+            assert torch.equal(getattr(m, x)[s, :len(rows)], before[x][s, rows])
+        for x in ("store", "merged"):
+            assert torch.equal(getattr(m, x)[s, :20], before[x][s, src[:20]])
+        for x in ("kp", "c"):
+            assert torch.equal(getattr(m, x)[s, 20 * B:new], before[x][s, n * B:length])
+        for x in ("k", "v", "kp", "c"):
+            getattr(other, x)[s, :len(rows)] = before[x][s, rows]
+        other.store[s, :20] = before["store"][s, src[:20]]
+    # and the next call reads the rearranged cache
+    outs = []
+    q, iq, iw = r(S, 7, G * HG, D), r(S, 7, G, H, 64), r(S, 7, G, H).float()
+    rows = {x: r(S, 7, *getattr(m, x).shape[2:]) for x in ("k", "v", "kp", "c")}
+    for x in (m, other):
+        for name, t in rows.items():
+            getattr(x, name)[:, new:new + 7] = t
+        out = torch.zeros_like(q)
+        sel, cnt = torch.empty((S, 7, G, 9), dtype=torch.int32, device=dev), torch.empty((S, 7, G), dtype=torch.int32, device=dev)
+        x.forward(new, q, iq, iw, sel, cnt, out)
+        Bd.sgqa_check()
+        outs.append((out, sel))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])

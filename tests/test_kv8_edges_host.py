@@ -1,0 +1,15 @@
+"""Host side of the 8-bit cache, of eviction and of what they share with the other calls, at their edges (no GPU)."""
+import pytest
+
+from sparse_long_context_sgqa_b200 import binding as Bd
+from sparse_long_context_sgqa_b200.binding import Params
+
+
+@pytest.mark.parametrize("size", [Bd.sgqa_workspace_size, Bd.sgqa_workspace_size_q8])
+@pytest.mark.parametrize("S,G", [(1, 1), (2, 2), (1, 4), (16, 4), (5, 3)])
+def test_a_workspace_serves_calls_of_fewer_queries(size, S, G):
+    # a model's workspace is made for its chunk and serves every shorter call; few queries are split further than many
+    p = Params(num_kv_groups=G, topk=9)
+    for ctx in (512, 40_000, 300_000):
+        sizes = [size(p, S, n, ctx) for n in (1, 2, 7, 16, 31, 32, 33, 40, 64, 200, 512)]
+        assert sizes == sorted(sizes), ctx

@@ -21,6 +21,11 @@ import torch
 from . import binding as Bd
 
 
+def _on(stream):
+    """Context in which torch's own work runs on the given stream, or the current one."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 class SparseGQA:
     def __init__(self, params: Bd.Params, num_seqs: int, capacity: int, chunk: int, device,
                  keep_merged_f32: bool = False, kv_dtype: str = "bf16", track_weights: bool = False):
@@ -89,11 +94,13 @@ class SparseGQA:
             Bd.sgqa_forward_gated(self.p, self.S, q_pos0, nq, q, idx_q, idx_w, self.cap, clen, self.kp, self.c,
                                   self.k, self.v, self.merged, self.store, sel, sel_count, gate, out, self.ws, stream)
 
-    def reset(self):
-        """Forget the accumulated weights and evictions: the next call starts new sequences at position 0."""
+    def reset(self, stream=None):
+        """Forget the accumulated weights and evictions: the next call starts new sequences at position 0.
+        The weights are cleared on the given stream, which should be the calls' (default: the current one)."""
         self.evicted = self.pos_count = 0
         if self.acc is not None:
-            self.acc.zero_()
+            with _on(stream):
+                self.acc.zero_()
 
     def evict(self, cache_len, keep, first=0, recent=0, acc=None, stream=None):
         """Keep `keep` of the complete blocks of cache_len tokens; returns the new cache length.
@@ -111,7 +118,7 @@ class SparseGQA:
             raise ValueError("evict needs accumulated weights: track_weights or acc=")
         if self.pos is None:
             # on the call's stream: memory that another stream's work still uses is not handed to it
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            with _on(stream):
                 self._evict_ws = Bd.alloc_evict_workspace(self.p, self.S, self.cap, self.device)
                 self.pos = torch.empty((self.S, self.cap // B), dtype=torch.int32, device=self.device)
         kv = [self.kv8, self.kv_scale] if self.kv_dtype == "e4m3" else [self.k, self.v]

@@ -1,6 +1,7 @@
 """Host side of the 8-bit cache, of eviction and of what they share with the other calls, at their edges (no GPU)."""
 import pytest
 
+from sparse_long_context_sgqa_b200 import api
 from sparse_long_context_sgqa_b200 import binding as Bd
 from sparse_long_context_sgqa_b200.binding import Params
 
@@ -13,3 +14,24 @@ def test_a_workspace_serves_calls_of_fewer_queries(size, S, G):
     for ctx in (512, 40_000, 300_000):
         sizes = [size(p, S, n, ctx) for n in (1, 2, 7, 16, 31, 32, 33, 40, 64, 200, 512)]
         assert sizes == sorted(sizes), ctx
+
+
+def test_reset_clears_the_weights_on_the_calls_stream(monkeypatch):
+    # the calls before it may still be adding weights on that stream
+    class On:
+        def __init__(self, st):
+            self.st = st
+
+        def __enter__(self):
+            cur.append(self.st)
+
+        def __exit__(self, *a):
+            cur.pop()
+
+    cur, seen = [], []
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 64, 8, "cpu", kv_dtype="e4m3", track_weights=True)
+    m.acc = type("Acc", (), {"zero_": lambda self: seen.append(list(cur))})()
+    monkeypatch.setattr(api.torch.cuda, "stream", On)
+    m.reset(stream="side")
+    m.reset()
+    assert seen == [["side"], []]

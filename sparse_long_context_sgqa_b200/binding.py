@@ -52,6 +52,8 @@ class _CacheArray(ctypes.Structure):
 
 @dataclasses.dataclass
 class Params:
+    __slots__ = ("_struct", "__dict__", "__weakref__")  # the C structure stays out of the fields' dictionary
+
     num_kv_groups: int = 4
     heads_per_group: int = 16
     head_dim: int = 192
@@ -64,15 +66,21 @@ class Params:
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        self.__dict__.pop("_struct", None)  # built again by the next call
+        object.__setattr__(self, "_struct", None)  # built again by the next call
 
     def c(self) -> _Params:
-        c = self.__dict__.get("_struct")
+        c = getattr(self, "_struct", None)
         if c is None:
             c = _Params(self.num_kv_groups, self.heads_per_group, self.head_dim, self.idx_heads, self.idx_dim,
                         self.block_size, self.topk, self.merge_in_f32, self.scale)
-            self.__dict__["_struct"] = c
+            object.__setattr__(self, "_struct", c)
         return c
+
+    def __getstate__(self):
+        return dict(self.__dict__)
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
 
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t

@@ -1,4 +1,8 @@
 """Host side of the 8-bit cache, of eviction and of what they share with the other calls, at their edges (no GPU)."""
+import copy
+import dataclasses
+import pickle
+
 import pytest
 
 from sparse_long_context_sgqa_b200 import api
@@ -35,3 +39,14 @@ def test_reset_clears_the_weights_on_the_calls_stream(monkeypatch):
     m.reset(stream="side")
     m.reset()
     assert seen == [["side"], []]
+
+
+def test_params_hold_their_fields_only():
+    # what a call keeps beside them is not one of them: copies by field, also after a call
+    p = Params(num_kv_groups=2, topk=7)
+    Bd.sgqa_workspace_size(p, 1, 1, 64)
+    assert Params(**vars(p)) == p and list(vars(p)) == [f.name for f in dataclasses.fields(Params)]
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p, topk=9)):
+        assert q.c().num_kv_groups == 2 and q.c().topk == q.topk
+        q.topk = 11
+        assert q.c().topk == 11 and p.c().topk == 7

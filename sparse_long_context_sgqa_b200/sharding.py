@@ -46,6 +46,17 @@ def shard_kv(k, v, num_groups: int, world: int, rank: int):
     return k[:, :, g0:g1].contiguous(), v[:, :, g0:g1].contiguous()
 
 
+def shard_heads(name, t, num_groups: int, per_group: int, world: int, rank: int):
+    """This rank's part of a tensor [S, N, G*per_group, ...] (contiguous); a tensor of the rank's own part is taken as it is."""
+    g0, g1 = group_range(num_groups, world, rank)
+    if t.shape[2] == num_groups * per_group:
+        return t[:, :, g0 * per_group:g1 * per_group].contiguous()
+    if t.shape[2] == (g1 - g0) * per_group:
+        return t
+    raise ValueError(f"{name}: expected {num_groups * per_group} entries in dimension 2, or this rank's "
+                     f"{(g1 - g0) * per_group}, got {tuple(t.shape)}")
+
+
 def gather_heads(local_out: torch.Tensor, world: int, group=None) -> torch.Tensor:
     """All-gather every rank's output heads [S, N, Gl*Hg, D] into the full
     [S, N, W*Gl*Hg, D], rank r's heads at their global position."""
@@ -85,8 +96,12 @@ class GroupShardedSGQA:
 
     def forward(self, q_pos0, q, idx_q, idx_w, gather: bool = True, **kw):
         """The path for this rank's groups on full query tensors; returns the
-        full output (all ranks' heads, gathered) or this rank's heads only."""
+        full output (all ranks' heads, gathered) or this rank's heads only.
+        gate ([S, N, G*Hg] logits) is sliced like the queries; other keywords
+        reach the model as they are."""
         Hg = self.full.heads_per_group
+        if kw.get("gate") is not None:
+            kw["gate"] = shard_heads("gate", kw["gate"], self.full.num_kv_groups, Hg, self.world, self.rank)
         ql, iql, iwl = shard_queries(q, idx_q, idx_w, self.full.num_kv_groups, Hg, self.world, self.rank)
         S, N = q.shape[0], q.shape[1]
         Gl = self.g1 - self.g0

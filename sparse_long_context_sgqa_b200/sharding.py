@@ -75,7 +75,9 @@ class GroupShardedSGQA:
     ``model`` is a SparseGQA-like object built with this rank's group count
     (``local_params``) whose ``forward(q_pos0, q, idx_q, idx_w, sel, sel_count,
     out, ...)`` runs the path on this rank's slices; its caches hold this
-    rank's K/V groups and the full proxy keys and logits.
+    rank's K/V groups and the full proxy keys and logits.  With the 8-bit cache
+    and tracked weights every rank's ``acc`` counts its own groups' heads, so
+    evictions by it differ from rank to rank, each from its own copy of the store.
     """
 
     def __init__(self, params, world: int, rank: int, make_model, group=None):
@@ -85,9 +87,18 @@ class GroupShardedSGQA:
         self.local_params = dataclasses.replace(params, num_kv_groups=self.g1 - self.g0)
         self.model = make_model(self.local_params)
 
-    def load_cache(self, kp, c, k, v):
-        """Fill this rank's caches from full-cache tensors (positions [0, L))."""
+    def load_cache(self, kp, c, k=None, v=None):
+        """Fill this rank's caches from full-cache tensors (positions [0, L)).
+        A model with the 8-bit cache takes its K/V rows with the calls: no k and v here."""
         L = kp.shape[1]
+        if getattr(self.model, "kv_dtype", "bf16") == "e4m3":
+            if k is not None or v is not None:
+                raise ValueError("the 8-bit cache takes K/V rows with the calls (forward(..., k=, v=)), not from load_cache")
+            self.model.kp[:, :L].copy_(kp)
+            self.model.c[:, :L].copy_(c)
+            return
+        if k is None or v is None:
+            raise ValueError("BF16 caches are loaded with k and v")
         kl, vl = shard_kv(k, v, self.full.num_kv_groups, self.world, self.rank)
         self.model.kp[:, :L].copy_(kp)
         self.model.c[:, :L].copy_(c)
@@ -97,11 +108,13 @@ class GroupShardedSGQA:
     def forward(self, q_pos0, q, idx_q, idx_w, gather: bool = True, **kw):
         """The path for this rank's groups on full query tensors; returns the
         full output (all ranks' heads, gathered) or this rank's heads only.
-        gate ([S, N, G*Hg] logits) is sliced like the queries; other keywords
-        reach the model as they are."""
+        gate ([S, N, G*Hg] logits) and the 8-bit cache's rows k and v
+        ([S, N, G, D]) are sliced like the queries; other keywords reach the
+        model as they are."""
         Hg = self.full.heads_per_group
-        if kw.get("gate") is not None:
-            kw["gate"] = shard_heads("gate", kw["gate"], self.full.num_kv_groups, Hg, self.world, self.rank)
+        for name, per_group in (("gate", Hg), ("k", 1), ("v", 1)):
+            if kw.get(name) is not None:
+                kw[name] = shard_heads(name, kw[name], self.full.num_kv_groups, per_group, self.world, self.rank)
         ql, iql, iwl = shard_queries(q, idx_q, idx_w, self.full.num_kv_groups, Hg, self.world, self.rank)
         S, N = q.shape[0], q.shape[1]
         Gl = self.g1 - self.g0

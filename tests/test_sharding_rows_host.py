@@ -34,3 +34,27 @@ def test_gate_of_the_ranks_heads(world, rank):
         sh.forward(0, *queries(), gather=False, gate=gate[:, :, 1:])
     sh.forward(0, *queries(), gather=False, gate=None, stream="side")
     assert calls[-1] == dict(gate=None, stream="side")
+
+
+@pytest.mark.parametrize("world,rank", [(1, 0), (2, 1), (4, 3)])
+def test_rows_of_the_8bit_cache(world, rank):
+    sh, m, calls = layer(world, rank, kv_dtype="e4m3")
+    kp, c, k, v = torch.randn(S, 9, DI), torch.randn(S, 9, DI), torch.randn(S, N, G, D), torch.randn(S, N, G, D)
+    sh.load_cache(kp, c)
+    assert torch.equal(m.kp[:, :9], kp) and torch.equal(m.c[:, :9], c) and not m.kp[:, 9:].any()
+    per = G // world
+    sh.forward(0, *queries(), gather=False, k=k, v=v)
+    for name, t in (("k", k), ("v", v)):
+        assert torch.equal(calls[-1][name], t[:, :, rank * per:(rank + 1) * per]) and calls[-1][name].is_contiguous()
+    # the rows come with the calls: there is no BF16 cache to load
+    with pytest.raises(ValueError, match="8-bit"):
+        sh.load_cache(kp, c, k, v)
+
+
+def test_bf16_caches_are_loaded_whole():
+    sh, m, _ = layer(2, 1, kv_dtype="bf16", k=torch.zeros(S, 16, 2, D), v=torch.zeros(S, 16, 2, D))
+    kp, c, k, v = torch.randn(S, 9, DI), torch.randn(S, 9, DI), torch.randn(S, 9, G, D), torch.randn(S, 9, G, D)
+    with pytest.raises(ValueError, match="k and v"):
+        sh.load_cache(kp, c)
+    sh.load_cache(kp, c, k, v)
+    assert torch.equal(m.k[:, :9], k[:, :, 2:]) and torch.equal(m.v[:, :9], v[:, :, 2:])

@@ -289,9 +289,11 @@ sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t ca
  * sgqa_sparse_attn_gated over the 8-bit cache.  Attention of the values
  * code * scale: a query's current block has one scale for all of its tokens
  * that are in the cache, the query's later ones among them.  Queries and softmax
- * weights are not rounded to 8 bits: a query value is carried as two E4M3 values
- * (exact down to 2^-11 of its head's largest), a weight to 2^-9 of itself and
- * down to 2^-27 of the row's largest.  Sums and softmax statistics are FP32.
+ * weights are not rounded to 8 bits.  A query value is carried as two E4M3
+ * values: exact down to 2^-9.8 of its head's largest and off by at most 2^-17.8
+ * of that below (calls of at most 32 queries per sequence: 2^-13.8 and 2^-21.8).
+ * A weight is carried to 2^-9 of itself and down to 2^-27 of the row's largest.
+ * Sums and softmax statistics are FP32.
  *
  * gate : [S, nq, G*Hg] bf16 gate logits, or NULL (no gate)
  * acc  : [S, cache_cap / 8] int64, or NULL.  Accumulated attention weight of

@@ -4,7 +4,8 @@
 //
 // A query is not rounded to 8 bits: it is split into two E4M3 values, x = hi +
 // lo / 16 with hi = E4M3(x), lo = E4M3(16 (x - hi)), which carry a BF16 value (8
-// significant bits) exactly over 2^13 of range below the row's largest.  Softmax
+// significant bits) exactly down to 2^-13.8 of the row's largest; below, a value
+// is off by at most 2^-21.8 of that (many queries: see there).  Softmax
 // weights need more range than E4M3 has: where one token takes most of a row (a
 // sink), the result lies in weights 2^-14 of the largest and below.  Few queries
 // split them into three E5M2 values (2^-9 of a weight, in FP16's range), many
@@ -622,8 +623,9 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 //               result lies in weights 2^-14 of the largest and below, which two
 //               E4M3 halves in one accumulator lose.
 // lo is not multiplied by 16 here (both halves add into one accumulator): a query
-// value is exact down to 2^-11 of the row's largest, smaller ones are off by at most
-// 2^-19 of it.
+// value is exact down to 2^-9.8 of the row's largest, smaller ones are off by at
+// most 2^-17.8 of it (half a step of the smallest E4M3 values, 2^-10, where the
+// largest is just above 224).
 // A block's K scale and the row's query scale multiply its scores; its V scale
 // enters the exponent (2^(s + log2 vs - ref)) and leaves the block's sum again.
 //

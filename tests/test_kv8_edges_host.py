@@ -4,6 +4,7 @@ import dataclasses
 import pickle
 
 import pytest
+import torch
 
 from sparse_long_context_sgqa_b200 import api
 from sparse_long_context_sgqa_b200 import binding as Bd
@@ -50,3 +51,18 @@ def test_params_hold_their_fields_only():
         assert q.c().num_kv_groups == 2 and q.c().topk == q.topk
         q.topk = 11
         assert q.c().topk == 11 and p.c().topk == 7
+
+
+@pytest.mark.parametrize("lo_scale,exact_from,off", [(16.0, 2.0 ** -13.8, 2.0 ** -21.8), (1.0, 2.0 ** -9.8, 2.0 ** -17.8)])
+def test_two_e4m3_values_carry_a_query_value(lo_scale, exact_from, off):
+    # every BF16 value under the scale that brings its row's largest into (224, 448], split as the kernels split it: few
+    # queries with the second value scaled by 16, many without.  Bounds as sgqa.h states them, for the least favourable
+    # largest value, 225 (the first BF16 value above 224).
+    x = torch.arange(0, 0x7F80, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16).double()
+    x = x[x <= 448]
+    code = lambda t: t.float().to(torch.float8_e4m3fn).double()  # noqa: E731
+    hi = code(x)
+    wrong = (hi + code((x - hi) * lo_scale) / lo_scale - x).abs()
+    assert not wrong[x >= 225 * exact_from].any()
+    assert wrong.max() <= 225 * off
+    assert wrong.max() >= 0.98 * 225 * off and wrong[x < 225 * exact_from].any()  # the bounds are tight

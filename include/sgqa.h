@@ -302,8 +302,10 @@ sgqa_status sgqa_kv_append_q8(const sgqa_params* p, int64_t num_seqs, int64_t ca
  *        tokens.  Integer sums: their order does not matter.  NaN weights add 0.
  *        Of a call that sgqa_check reports as SGQA_ERR_TIMEOUT a part of the
  *        weights, possibly none, has been added.
- * sel ids must be strictly ascending and below floor(t/8); others are left out
- * and reported by sgqa_check as SGQA_ERR_DEVICE.
+ * sel ids must be strictly ascending and in [0, floor(t/8)).  An id outside that
+ * range is left out and reported by sgqa_check as SGQA_ERR_DEVICE.  Calls of at
+ * most 32 queries per sequence do the same with an id that is not above the one
+ * before it in the list; calls of more take the list as a set.
  * kv_scale: as sgqa_kv_append_q8 writes it: positive (or NaN), at least 2^-100.
  * Rows of a block at positions >= cache_len must not hold the E4M3 NaN codes
  * 0x7F and 0xFF (sgqa_kv_append_q8 writes code 0 there).

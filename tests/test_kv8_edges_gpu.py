@@ -195,6 +195,28 @@ def test_threads_with_contexts_of_different_length(Bd, cuda_device):
     assert all(torch.equal(j["out"], w) for j, w in zip(jobs, want))
 
 
+# ------------------ lists that break the contract
+@pytest.mark.parametrize("nq", [1, 40])
+def test_repeated_and_unordered_ids(Bd, cuda_device, nq):
+    # few queries leave out (and report) an id that is not above the one before it; many attend the set of the list
+    c = T.make_attn(1, 1, nq, 400, 8, cuda_device)
+    for i in range(nq):
+        c["sel"][0, i, 0] = torch.tensor([3, 9, 9, 20, 30, 25, 31, 40], dtype=torch.int32)
+    out = T.run_attn(Bd, c, check=False)
+    if nq <= 32:
+        with pytest.raises(Bd.SgqaError) as e:
+            Bd.sgqa_check()
+        assert e.value.code == 6
+        ids = [3, 9, 20, 30, 31, 40]
+    else:
+        Bd.sgqa_check()
+        ids = [3, 9, 20, 25, 30, 31, 40]
+    c["sel"][0, :, 0, :len(ids)] = torch.tensor(ids, dtype=torch.int32, device=cuda_device)
+    c["cnt"].fill_(len(ids))
+    ref, tol, _ = T.reference(c)
+    T.check_attn(c, out, ref, tol)
+
+
 # ------------------ a BF16 cache
 def test_evict_a_bf16_cache_by_given_weights(Bd, cuda_device):
     from sparse_long_context_sgqa_b200.api import SparseGQA

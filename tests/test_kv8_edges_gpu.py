@@ -195,6 +195,49 @@ def test_threads_with_contexts_of_different_length(Bd, cuda_device):
     assert all(torch.equal(j["out"], w) for j, w in zip(jobs, want))
 
 
+# ------------------ NaN blocks, weights
+def row_weights(c, s, i, g):
+    """Weights [blocks] that the heads of one (query, group) give."""
+    n = lambda t: t.cpu().double().numpy()  # noqa: E731
+    hs = slice(g * HG, (g + 1) * HG)
+    return R.attention(n(c["q"][s:s + 1, i:i + 1, hs]), R.codes_to_values(c["kv8"][s:s + 1, :, g:g + 1]),
+                       n(c["sc"][s:s + 1, :, g:g + 1]), c["sel"][s:s + 1, i:i + 1, g:g + 1].cpu().numpy(),
+                       c["cnt"][s:s + 1, i:i + 1, g:g + 1].cpu().numpy(), c["q0"] + i)[2][0]
+
+
+@pytest.mark.parametrize("nq", [1, 2, 40])
+@pytest.mark.parametrize("current", [False, True])
+def test_weights_beside_nan_blocks(Bd, cuda_device, nq, current):
+    # K with a NaN: the weights of every (query, group) that attends the block are NaN and not counted; V with one: the
+    # weights are as ever
+    c = T.make_attn(2, 2, nq, 1001, 50, cuda_device)
+    bad_k, bad_v = (1001 // B, 1001 // B) if current else (37, 42)
+    if not current:
+        c["sel"][0, 0, 0, 0], c["sel"][0, 0, 1, 0] = bad_k, bad_v
+    c["sel"] = c["sel"].sort(-1).values  # (k = 50 of 125 blocks: all lists are full)
+    for s in range(2):  # an id set twice moves on to a free one
+        for i in range(nq):
+            for g in range(2):
+                ids = sorted(set(c["sel"][s, i, g].tolist()))
+                free = (x for x in range(125) if x not in ids)
+                while len(ids) < 50:
+                    ids.append(next(free))
+                c["sel"][s, i, g] = torch.tensor(sorted(ids), dtype=torch.int32)
+    want = np.zeros((2, c["cap"] // B))
+    for s in range(2):
+        for i in range(nq):
+            for g in range(2):
+                hit = s == 0 and g == 0 and ((c["q0"] + i) // B == bad_k or bool((c["sel"][s, i, g] == bad_k).any()))
+                if not hit:
+                    want[s] += row_weights(c, s, i, g)
+    c["sc"][0, bad_k, 0, 0] = float("nan")
+    c["sc"][0, bad_v, 1, 1] = float("nan")
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    out = T.run_attn(Bd, c, acc=acc)
+    T.check_weights(acc, 0, want, nq * 2 * 2)
+    assert torch.isnan(out[0, 0]).all() and not torch.isnan(out[1]).any()
+
+
 # ------------------ lists that break the contract
 @pytest.mark.parametrize("nq", [1, 40])
 def test_repeated_and_unordered_ids(Bd, cuda_device, nq):
@@ -215,6 +258,65 @@ def test_repeated_and_unordered_ids(Bd, cuda_device, nq):
     c["cnt"].fill_(len(ids))
     ref, tol, _ = T.reference(c)
     T.check_attn(c, out, ref, tol)
+
+
+# ------------------ the softmax scale
+@pytest.mark.parametrize("nq", [1, 7, 40])
+@pytest.mark.parametrize("scale", [0.03125, 0.2])
+def test_softmax_scale(Bd, cuda_device, nq, scale):
+    c = T.make_attn(2, 2, nq, 1003, 60, cuda_device)
+    n = lambda t: t.cpu().double().numpy()  # noqa: E731
+    ref, tol, weights = R.attention(n(c["q"]) * (float(np.float32(scale)) * math.sqrt(D)), R.codes_to_values(c["kv8"]), n(c["sc"]),
+                                    c["sel"].cpu().numpy(), c["cnt"].cpu().numpy(), c["q0"])
+    p = Params(num_kv_groups=2, topk=60, scale=scale)
+    out = torch.zeros_like(c["q"])
+    acc = torch.zeros((2, c["cap"] // B), dtype=torch.int64, device=cuda_device)
+    ws = Bd.alloc_workspace_q8(p, 2, nq, 1003 + nq, cuda_device)
+    Bd.sgqa_sparse_attn_q8(p, 2, c["q0"], nq, c["q"], c["cap"], c["clen"], c["kv8"], c["sc"], c["sel"], c["cnt"], out, ws, acc=acc)
+    Bd.sgqa_check()
+    T.check_attn(c, out, ref, tol)
+    T.check_weights(acc, 0, weights, nq * 2 * 2)
+
+
+# ------------------ sinks
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("strength", [12.0, 16.0])
+def test_a_sink_leaves_the_others_weights(Bd, cuda_device, nq, strength):
+    """One token with V = 0 takes e^strength of every other token's weight; the result lies in the others.
+
+    A weight's rounding is off by at most 2^-9 of it (three E5M2 values; FP16: 2^-11), 2^-14 for its score, and 2^-27 of
+    the largest weight of the row; the roundings of different tokens have nothing to do with one another, so the errors'
+    mean square is at most the sum of the squares of these bounds times the values.  The result's own rounding: 2^-8 of it."""
+    c = T.make_attn(1, 2, nq, 4001, 500, cuda_device, sigma=0.2)
+    c["sel"][..., 0] = 0
+    c["q"][..., 0] = 4.0
+    one = torch.tensor(448.0).to(torch.float8_e4m3fn).view(torch.uint8).to(cuda_device)
+    c["kv8"][:, :, :, 0, :, 0] = 0
+    c["kv8"][:, 0, :, :, 3] = 0
+    c["kv8"][:, 0, :, 0, 3, 0] = one
+    c["sc"][:, :, :, 0] = 2.0 ** -10
+    c["sc"][:, 0, :, 0] = strength * 192 ** 0.5 / (448 * 4)
+    c["sc"][:, :, :, 1] = 2.0 ** -8
+    got = T.run_attn(Bd, c, gate=False)[0].cpu().double().numpy()
+    err = square = size = 0.0
+    for i in range(nq):
+        t = c["q0"] + i
+        for g in range(2):
+            ids = c["sel"][0, i, g, :c["cnt"][0, i, g]].tolist() + [t // B]
+            n = len(ids) * B - (B - 1 - t % B)
+            K, V = ((R.codes_to_values(c["kv8"][0, ids, g, x]) * c["sc"][0, ids, g, x].cpu().double().numpy()[:, None, None])
+                    .reshape(-1, D)[:n] for x in (0, 1))
+            hs = slice(g * HG, (g + 1) * HG)
+            s = c["q"][0, i, hs].cpu().double().numpy() @ K.T / math.sqrt(D)
+            w = np.exp(s - s.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            off = (2.0 ** -9 + 2.0 ** -14) * w + 2.0 ** -27 * w.max(1, keepdims=True)
+            err += ((got[i, hs] - w @ V) ** 2).sum()
+            square += (off ** 2 @ V ** 2).sum()
+            size += ((w @ V) ** 2).sum()
+    err, bound, size = math.sqrt(err), math.sqrt(square) + 2.0 ** -8 * math.sqrt(size), math.sqrt(size)
+    assert bound < size / 4  # (zeros would not pass)
+    assert err <= bound, (err, bound, size)
 
 
 # ------------------ a BF16 cache

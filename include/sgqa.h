@@ -275,7 +275,10 @@ sgqa_status sgqa_sparse_attn_paged(const sgqa_params* p, int64_t num_seqs, int64
  * earlier call takes its older rows from `tail` and is quantised again, so
  * the cache depends on the rows alone, not on how they were cut into calls.
  * `tail` is left with the rows of block floor((pos0 + n) / 8); it may be NULL
- * where both pos0 and pos0 + n are multiples of 8.  A block whose K (or V)
+ * where both pos0 and pos0 + n are multiples of 8.  A call may begin at an
+ * earlier position again (drafted tokens that were not kept): inside the block
+ * whose rows tail holds, or at a multiple of 8; elsewhere the block's older rows
+ * are gone and it would be quantised from another's.  A block whose K (or V)
  * holds an infinity or NaN gets scale NaN and codes 0 there: every query that
  * attends it reads NaN, no other is touched.
  *

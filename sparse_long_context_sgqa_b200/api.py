@@ -64,6 +64,16 @@ class SparseGQA:
         self.evicted = 0        # blocks of a sequence evicted so far
         self.pos_count = 0      # slots whose original block number `pos` holds
         self.pos = self._evict_ws = None
+        # 8-bit cache: tokens it holds after the last call; None: not known (nothing called yet, a cache filled by
+        # hand, a captured call), and where a call begins is not checked
+        self.length = None
+
+    def _check_tail(self, at):
+        """The 8-bit cache's incomplete block is quantised from its BF16 rows; tail holds those of one block only."""
+        if at % 8 and self.length is not None and not (at // 8 == self.length // 8 and at <= self.length):
+            raise ValueError(f"position {at} lies inside a block whose rows are not in tail, which holds those of positions "
+                             f"{self.length // 8 * 8} to {self.length - 1}: go back to a multiple of 8 and append from there "
+                             "(or set .length, if the cache was filled outside these calls)")
 
     def forward(self, q_pos0, q, idx_q, idx_w, sel, sel_count, out, cache_len=None, stream=None, gate=None, k=None,
                 v=None):
@@ -72,7 +82,11 @@ class SparseGQA:
         Every tensor is contiguous with the layouts of include/sgqa.h; gate
         ([S, nq, G*Hg] bf16 logits) applies the head-wise sigmoid output gate.
         With the 8-bit cache k and v ([S, nq, G, D] bf16) are the call's own
-        rows, and the cache holds q_pos0 + nq tokens after it.
+        rows, and the cache holds q_pos0 + nq tokens after it.  A call may take
+        back tokens (drafts that were not accepted) by a smaller q_pos0: one
+        inside the block that the last call ended in, or a multiple of 8, from
+        which that block's rows are given again; others are refused.  Tracked
+        weights keep what the tokens taken back have added.
         """
         nq = q.shape[1]
         if self.kv_dtype == "e4m3":
@@ -80,9 +94,16 @@ class SparseGQA:
                 raise ValueError("the 8-bit cache takes the call's K/V rows: forward(..., k=, v=)")
             if cache_len is not None and cache_len != q_pos0 + nq:
                 raise ValueError("the 8-bit cache ends with the call's own rows: cache_len is q_pos0 + nq")
+            if nq:
+                self._check_tail(q_pos0)
+            before, self.length = self.length, None
             Bd.sgqa_forward_q8(self.p, self.S, q_pos0, nq, q, idx_q, idx_w, self.cap, self.kp, self.c, k, v, self.tail,
                                self.kv8, self.kv_scale, self.merged, self.store, sel, sel_count, out, self.ws, gate=gate,
                                acc=self.acc, stream=stream)
+            if nq == 0:
+                self.length = before
+            elif not (self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()):
+                self.length = q_pos0 + nq
             return
         if k is not None or v is not None:
             raise ValueError("with BF16 caches the call's K/V rows are already in .k and .v")
@@ -98,6 +119,7 @@ class SparseGQA:
         """Forget the accumulated weights and evictions: the next call starts new sequences at position 0.
         The weights are cleared on the given stream, which should be the calls' (default: the current one)."""
         self.evicted = self.pos_count = 0
+        self.length = None
         if self.acc is not None:
             with _on(stream):
                 self.acc.zero_()
@@ -108,7 +130,8 @@ class SparseGQA:
         The blocks with the largest accumulated weight stay (acc: [S, capacity / B]
         int64, rearranged in place; where weights are tracked it is those), and in any
         case the `first` first and `recent` last blocks of the sequence.  The
-        next call's q_pos0 is the returned length.
+        next call's q_pos0 is the returned length.  The counts that go with an
+        eviction are the host's: a captured one is replayed once at most.
         """
         B = self.p.block_size
         if acc is not None and self.acc is not None and acc is not self.acc:
@@ -116,6 +139,8 @@ class SparseGQA:
         acc = self.acc if acc is None else acc
         if acc is None:
             raise ValueError("evict needs accumulated weights: track_weights or acc=")
+        if self.kv_dtype == "e4m3":
+            self._check_tail(cache_len)
         if self.pos is None:
             # on the call's stream: memory that another stream's work still uses is not handed to it
             with _on(stream):
@@ -129,6 +154,8 @@ class SparseGQA:
                       tail_arrays=[self.kp, self.c], stream=stream)
         self.evicted += n - keep
         self.pos_count = keep
+        if self.length is not None:
+            self.length = keep * B + cache_len % B
         return keep * B + cache_len % B
 
     def prefill(self, q, idx_q, idx_w, out, sel=None, sel_count=None, q_pos0=0, stream=None, gate=None, k=None, v=None):

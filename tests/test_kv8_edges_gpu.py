@@ -366,3 +366,19 @@ def test_evict_a_bf16_cache_by_given_weights(Bd, cuda_device):
         Bd.sgqa_check()
         outs.append((out, sel))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ------------------ a shorter call after a longer one
+def test_drafts_taken_back_within_the_block(Bd, cuda_device):
+    # five tokens, of which the last three are replaced: `tail` holds the rows before them
+    G, dev = 2, cuda_device
+    k, v = T.rows(1, 21, G, 1), T.rows(1, 21, G, 2)
+    p = Params(num_kv_groups=G)
+    kv8, sc, tail = T.empty_cache(1, 4, G, dev)
+    junk_k, junk_v = T.rows(1, 3, G, 3) * 50, T.rows(1, 3, G, 4) * 50
+    T.append(Bd, p, 1, 32, [17], k, v, kv8, sc, tail, dev)
+    Bd.sgqa_kv_append_q8(p, 1, 32, 17, 5, torch.cat([k[:, 17:19], junk_k], 1).to(dev), torch.cat([v[:, 17:19], junk_v], 1).to(dev),
+                         tail, kv8, sc)
+    Bd.sgqa_kv_append_q8(p, 1, 32, 19, 2, k[:, 19:].to(dev), v[:, 19:].to(dev), tail, kv8, sc)
+    Bd.sgqa_check()
+    T.check_cache(k, v, 21, kv8, sc, tail)

@@ -66,3 +66,62 @@ def test_two_e4m3_values_carry_a_query_value(lo_scale, exact_from, off):
     assert not wrong[x >= 225 * exact_from].any()
     assert wrong.max() <= 225 * off
     assert wrong.max() >= 0.98 * 225 * off and wrong[x < 225 * exact_from].any()  # the bounds are tight
+
+
+def _tokens(m, monkeypatch):
+    """m.forward and m.evict without a GPU: forward(position, tokens)."""
+    monkeypatch.setattr(Bd, "sgqa_forward_q8", lambda *a, **kw: None)
+    monkeypatch.setattr(Bd, "sgqa_evict", lambda *a, **kw: None)
+
+    def forward(pos, n):
+        x = torch.zeros((1, n, 1, 192), dtype=torch.bfloat16)
+        m.forward(pos, x, None, None, None, None, None, k=x, v=x)
+    return forward
+
+
+def test_tokens_taken_back_need_the_rows_of_their_block(monkeypatch):
+    # `tail` holds the rows of the block that the last call ended in: a call that begins inside another one would quantise
+    # that block from rows of a different block
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 256, 8, "cpu", kv_dtype="e4m3", track_weights=True)
+    forward = _tokens(m, monkeypatch)
+    forward(13, 3)                       # a cache filled by hand: nothing is known of tail
+    assert m.length == 16
+    forward(16, 7)                       # drafts, of which three stay
+    forward(19, 7)                       # 19 .. 25: into the next block
+    for pos in (20, 23, 27, 29):         # in the block before, and behind the cache's end
+        with pytest.raises(ValueError, match="tail"):
+            forward(pos, 1)
+        assert m.length == 26
+    with pytest.raises(ValueError, match="tail"):
+        m.evict(21, 1)
+    forward(25, 1)                       # inside the block that tail holds
+    forward(16, 9)                       # a whole block again, from its first row
+    assert m.evict(24, 2) == 16          # (whole blocks need no rows)
+    forward(16, 3)
+    assert m.evict(19, 1) == 11
+    forward(11, 1)
+    m.length = None                      # filled outside these calls
+    forward(21, 1)
+    m.reset()
+    assert m.length is None
+
+
+def test_a_call_that_failed_leaves_the_length_unknown(monkeypatch):
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 256, 8, "cpu", kv_dtype="e4m3")
+    forward = _tokens(m, monkeypatch)
+    forward(0, 5)
+
+    def fails(*a, **kw):
+        raise Bd.SgqaError(2, "")
+    monkeypatch.setattr(Bd, "sgqa_forward_q8", fails)
+    with pytest.raises(Bd.SgqaError):
+        forward(5, 1)
+    assert m.length is None
+
+
+def test_bf16_caches_take_tokens_back_anywhere(monkeypatch):
+    monkeypatch.setattr(Bd, "sgqa_forward", lambda *a, **kw: None)
+    m = api.SparseGQA(Params(num_kv_groups=1), 1, 256, 8, "cpu")
+    x = torch.zeros((1, 7, 16, 192), dtype=torch.bfloat16)
+    for pos in (19, 21, 3, 40):
+        m.forward(pos, x, None, None, None, None, None)

@@ -87,8 +87,8 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
 // after the softmax of its tile.  The splits of a row form one cluster and
 // combine through distributed shared memory.
 // Measured, in a CUDA graph: 16 contexts of 262144 tokens, 512 blocks each, 28.0 us
-// (the bytes at the copy rate: 15.5 us), 16 x 32768 with gate and weights 32.9 us,
-// one query at position 1024 8.6 us.  Of the last little is bytes: lists, scales,
+// (the bytes at the copy rate: 15.5 us), 16 x 32768 with gate and weights 32.0 us,
+// one query at position 1024 8.8 us.  Of the last little is bytes: lists, scales,
 // gather, two products and combine follow one another.
 // ---------------------------------------------------------------------------
 constexpr int kQdTile = 16;       // blocks per tile
@@ -633,7 +633,7 @@ attn_q8_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __nv_bflo
 // row's log-sum known, S alone is computed again, and each block's weights are
 // summed over the unit's 128 rows, eight blocks of a tile at a time.
 // Measured, in a CUDA graph with the plan of the unions: 2048 queries at 8192, 512
-// blocks each, 555-564 us; 2 x 1001 queries with gate and weights 531 us.  Bound by
+// blocks each, 553-564 us; 2 x 1001 queries with gate and weights 532 us.  Bound by
 // the softmax warps' issue and latency: the tensor pipe is active 43% of the time.
 // Sixteen softmax warps (575 us) and a maximum taken ahead of the exponentials (580
 // us) were slower than this form in the same run (558 us).

@@ -34,8 +34,9 @@ constexpr int kAppendWarps = 8;
 // A block that holds an infinity or NaN gets scale NaN and codes 0: whoever
 // attends it reads NaN, nobody else is touched.
 // Bound: HBM, 2 bytes read and 1 written per element.  Measured, in a CUDA graph:
-// 8192 tokens 8.0 us (4.7 TB/s; 5.8 us at the copy rate), 3 x 1001 tokens 3.9 us,
-// 16 sequences x 1 token 2.7 us (launch); a host call takes 16 us in all three.
+// 8192 tokens 8.0 us (4.7 TB/s; 5.8 us at the copy rate), 3 x 1001 tokens 4.0 us,
+// 16 sequences x 1 token 2.7 us (launch); the call from Python takes 8 to 11 us of
+// host time in all three.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kAppendWarps * 32)
 kv_append_q8_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
